@@ -29,6 +29,9 @@
  *   dense batched bf16 varlen_attn_fwd_dense / _bwd_dense ([B, S, H, D]);
  *   E4M3 (FP8) forward varlen_attn_fwd_fp8, _fp8_window, _fp8_dense (D = 128,
  *                      quantised from bf16 into a caller workspace);
+ *   paged cache        varlen_attn_cache_write / _cache_read (bf16 or E4M3
+ *                      pages), varlen_attn_fwd_paged (+ _workspace_size),
+ *                      grouped heads, single tokens to long chunks;
  *   status             varlen_attn_get_device_status, _status_string,
  *                      _last_cuda_error;
  *   diagnostics        tile counts and schedules, the bounded-wait self test,
@@ -305,6 +308,120 @@ int varlen_attn_fwd_fp8_dense(const void* q, varlen_dense_stride sq, const void*
                               int32_t seqlen_k, int32_t num_heads, int32_t head_dim, float scale, int32_t causal,
                               void* out, varlen_dense_stride so, float* lse, void* workspace, size_t workspace_bytes,
                               void* stream);
+
+/*
+ * Paged key/value cache, and the attention that reads it (not on the pages: a
+ * plain extension for programs that generate; the conventions are those of
+ * the packed calls above).
+ *
+ * A cache holds the keys and values of many sequences in pages of page_size
+ * rows: key (page p, row r, head h, dim d) lives at
+ * k + p*sk.page + r*sk.row + h*sk.head + d (elements; values likewise).
+ * Position t of sequence b is row t % page_size of the page
+ * block_table[b*table_stride + t / page_size]; sequence b holds seqlens[b]
+ * positions.  block_table and seqlens are device int32 arrays that the host
+ * never reads; device code clamps seqlens[b] into [0, max_pages * page_size]
+ * and never follows an entry outside [0, num_pages): a write there is
+ * dropped, a read gives zero rows, and the call records
+ * VARLEN_ERR_DEVICE_BOUNDS (varlen_attn_get_device_status).  Sequences may
+ * share pages that nothing writes.
+ *
+ * type VARLEN_CACHE_BF16: bf16 elements, k_scale = v_scale = NULL.
+ * type VARLEN_CACHE_E4M3: one-byte E4M3 codes and a bf16 scale for every
+ * (page, head, row), k_scale[(p*num_kv_heads + h)*page_size + r]; an element
+ * is code * scale.  The scale is the least power of two s >= 2^-127 with
+ * amax <= 448 s over the head_dim elements (1 for a vector of zeros), the
+ * code x / s rounded to nearest even.  A vector that holds an infinity or a
+ * NaN is held as NaN: scale NaN, codes 0.  A power of two costs the codes no
+ * relative precision, and code * scale is exact in bf16 (where it neither
+ * overflows nor falls below bf16's normal range).
+ *
+ * k, v and the scales are 16-byte aligned; the strides are non-negative
+ * multiples of 16 bytes below 2^40 bytes, and the (page, row, head) vectors
+ * must not overlap (ordering the dimensions of extent > 1 by stride, the
+ * smallest is at least head_dim and each further one at least the previous
+ * extent times the previous stride; VARLEN_ERR_STRIDE).  page_size is a power
+ * of two from 16 to 1024, num_pages >= 1, max_pages * page_size < 2^31.  The
+ * struct itself is host memory, read during the call only.
+ */
+enum { VARLEN_CACHE_BF16 = 0, VARLEN_CACHE_E4M3 = 1 };
+
+typedef struct {
+  int64_t page;
+  int64_t row;
+  int64_t head;
+} varlen_page_stride;
+
+typedef struct {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  const int32_t* block_table; /* [batch] rows of max_pages entries */
+  const int32_t* seqlens;     /* [batch] */
+  varlen_page_stride sk;
+  varlen_page_stride sv;
+  int64_t table_stride;       /* entries between the rows of block_table */
+  int32_t type;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t max_pages;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+} varlen_kv_cache;
+
+/*
+ * Writes packed new rows into the cache.  k and v are NHD bf16
+ * [total, num_kv_heads, head_dim]; row i of segment b of cu_seqlens (n_b
+ * rows) goes to position seqlens[b] - n_b + i: seqlens counts the rows that
+ * the sequence holds after the call, the new ones last.  Rows whose position
+ * would be negative, and rows outside every segment, are not written.  Two
+ * rows that name the same place of the same page race.
+ */
+int varlen_attn_cache_write(const void* k, varlen_stride sk, const void* v, varlen_stride sv,
+                            const int32_t* cu_seqlens, int32_t batch, int32_t total, const varlen_kv_cache* cache,
+                            void* stream);
+
+/*
+ * Reads the cache back into packed bf16 rows, for the packed entry points:
+ * row i of segment b receives position seqlens[b] - n_b + i (rounded once
+ * from code * scale in an E4M3 cache).  Rows whose position would be negative
+ * are set to zero; rows outside every segment are not written.
+ */
+int varlen_attn_cache_read(const varlen_kv_cache* cache, const int32_t* cu_seqlens, int32_t batch, int32_t total,
+                           void* k, varlen_stride sk, void* v, varlen_stride sv, void* stream);
+
+/*
+ * Forward over the cache: packed queries q [total_q, num_heads, head_dim]
+ * (bf16, cu_seqlens_q) against all seqlens[b] positions of their sequence.
+ * num_heads is a multiple of the cache's num_kv_heads and at most 128 times
+ * it (VARLEN_ERR_SHAPE); query head h reads key head
+ * h / (num_heads / num_kv_heads).  The band, out and lse are those of
+ * varlen_attn_fwd_window with Sk = seqlens[b]: (-1, -1) no mask, (-1, 0)
+ * causal with the last query at the last key, so after
+ * varlen_attn_cache_write of the same rows each sees itself and what came
+ * before.  A row that sees no key gets O = 0 and LSE = -inf.  Cache rows that
+ * no query of a segment sees may hold anything, NaN included; cache and
+ * query values that are seen are assumed finite, as in the packed calls.
+ *
+ * max_seqlen_q chooses kernels only and is never trusted for correctness:
+ * when it is positive and max_seqlen_q * num_heads / num_kv_heads is at most
+ * 64, the kernel for few rows takes every segment; otherwise each segment is
+ * taken by the kernel that its own length calls for.
+ *
+ * q's strides must be positive where its extents are above 1.  `workspace`
+ * is caller scratch of varlen_attn_fwd_paged_workspace_size() bytes, 256-byte
+ * aligned, whose contents on entry do not matter (partial results of long
+ * sequences that several CTAs share; calls that overlap on the GPU need one
+ * each).  Results do not depend on anything but the inputs: partial results
+ * are joined in a fixed order.
+ */
+size_t varlen_attn_fwd_paged_workspace_size(int32_t batch, int32_t total_q, int32_t num_heads, int32_t num_kv_heads,
+                                            int32_t head_dim);
+int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int32_t* cu_seqlens_q, int32_t batch,
+                          int32_t total_q, int32_t num_heads, int32_t max_seqlen_q, const varlen_kv_cache* cache,
+                          float scale, int32_t window_left, int32_t window_right, void* out, varlen_stride so,
+                          float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Backward without a workspace argument, for callers that cannot allocate

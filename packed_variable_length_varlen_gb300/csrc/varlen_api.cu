@@ -21,6 +21,7 @@
 
 #include "varlen_attn.h"
 #include "varlen_internal.h"
+#include "varlen_paged.h"
 
 namespace varlen {
 
@@ -142,6 +143,14 @@ int device_info(DeviceInfo* out) {
 int device_ready() {
   DeviceInfo d;
   return device_info(&d);
+}
+
+int launch_device(int* sms, unsigned int** err) {
+  DeviceInfo d;
+  const int st = device_info(&d);
+  *sms = d.sms;
+  *err = d.err;
+  return st;
 }
 
 namespace {
@@ -300,6 +309,28 @@ void fp8_sections(int32_t batch, int32_t total_q, int32_t total_k, int32_t H, si
 }
 
 }  // namespace
+
+int check_nhd(const void* ptr, varlen_stride s, int64_t rows, int32_t H, int32_t D, bool output) {
+  return output ? check_output(ptr, s, rows, H, D) : check_operand(ptr, s, rows, H, D);
+}
+
+int encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                 const cuuint64_t* byte_strides, const cuuint32_t* box, bool swizzle) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return VARLEN_ERR_CUDA;
+  cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
+  CUresult r = enc(map, type, (cuuint32_t)rank, const_cast<void*>(base), dims, byte_strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? VARLEN_OK : VARLEN_ERR_STRIDE;
+}
+
+Span checked_span(const void* base, int64_t bytes) { return flat_span(base, bytes); }
+
+Span nhd_bytes(const void* base, varlen_stride s, int64_t rows, int32_t H, int32_t D) {
+  return nhd_span(base, s, rows, H, D);
+}
+
 }  // namespace varlen
 
 using namespace varlen;

@@ -1,0 +1,114 @@
+// varlen_paged.h -- launch structs of the paged key/value cache (write, read)
+// and of the attention over it, and the device helpers that resolve a cache
+// position to its page.
+#pragma once
+
+#include "varlen_attn.h"
+#include "varlen_internal.h"
+#include "varlen_sched.cuh"
+
+namespace varlen {
+
+// ------------------------------------------------- from varlen_api.cu
+// SM count and error word of the current device (VARLEN_ERR_ARCH elsewhere).
+int launch_device(int* sms, unsigned int** err);
+// Argument checks of one NHD operand, as input and as output.
+int check_nhd(const void* ptr, varlen_stride s, int64_t rows, int32_t H, int32_t D, bool output);
+// A tiled tensor map of `rank` dimensions (128-byte swizzle or none), 64-bit extents.
+int encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                 const cuuint64_t* byte_strides, const cuuint32_t* box, bool swizzle);
+// [base, base + bytes), shortened by the bounds checker's self test.
+Span checked_span(const void* base, int64_t bytes);
+// The bytes an NHD bf16 operand occupies.
+Span nhd_bytes(const void* base, varlen_stride s, int64_t rows, int32_t H, int32_t D);
+
+// ------------------------------------------------- the cache
+struct PageView {
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* seqlens;
+  int32_t num_pages, max_pages, page_size, page_shift;
+};
+
+// Positions sequence b holds, clamped to what its table row can name.
+__device__ __forceinline__ int32_t cache_len(const PageView& c, int32_t b) {
+  const int64_t cap = (int64_t)c.max_pages << c.page_shift;
+  return (int32_t)min((int64_t)max(__ldg(c.seqlens + b), 0), cap);
+}
+
+// Page that holds positions [i << page_shift, ...) of sequence b, 0 <= i <
+// max_pages; num_pages (no page: recorded as an error) for an entry that
+// names none.
+__device__ __forceinline__ int32_t page_at(const PageView& c, int32_t b, int32_t i, unsigned int* err) {
+  const int32_t id = __ldg(c.table + (int64_t)b * c.table_stride + i);
+  if ((uint32_t)id < (uint32_t)c.num_pages) return id;
+  if (err != nullptr) atomicOr(err, (unsigned int)kErrBounds);
+  return c.num_pages;
+}
+
+// The last segment b with cu[b] <= row (cu non-decreasing; any array gives
+// some b in [0, batch)), found by the whole warp 32 entries at a time.
+__device__ __forceinline__ int32_t warp_find_segment(const int32_t* cu, int32_t batch, int32_t total, int32_t row) {
+  int32_t lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int32_t step = (hi - lo + 31) / 32;
+    const int64_t i = (int64_t)lo + (int64_t)(threadIdx.x & 31) * step;
+    const bool below = i < hi && clamp_row(__ldg(cu + i), total) <= row;
+    const unsigned m = __ballot_sync(0xffffffffu, below);
+    const int32_t k = m == 0 ? 0 : 31 - __clz(m);
+    lo += k * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+struct CacheParams {
+  const __nv_bfloat16 *k_new, *v_new;  // write: the new rows
+  __nv_bfloat16 *k_out, *v_out;        // read: where the rows go
+  int64_t k_rs, k_hs, v_rs, v_hs;      // packed rows
+  uint8_t *k, *v;                      // pages
+  int64_t k_page, k_row, k_head, v_page, v_row, v_head;  // byte strides of the pages
+  __nv_bfloat16 *k_scale, *v_scale;    // E4M3 only
+  PageView pages;
+  const int32_t* cu;
+  int32_t batch, total, heads;
+  unsigned int* err;
+  Span k_span, v_span, kp_span, vp_span, ks_span, vs_span;  // packed rows, pages, scales (bounds-checking build)
+};
+
+struct CacheLaunch {
+  CacheParams p;
+  int head_dim;
+  bool e4m3, write;
+};
+
+cudaError_t launch_cache(const CacheLaunch& L, cudaStream_t stream);
+
+// ------------------------------------------------- attention over the cache
+struct PagedParams {
+  const __nv_bfloat16* q;
+  int64_t q_rs, q_hs;
+  __nv_bfloat16* out;
+  int64_t o_rs, o_hs;
+  float* lse;
+  const uint8_t *k, *v;
+  int64_t k_page, k_row, k_head, v_page, v_row, v_head;  // byte strides of the pages
+  const __nv_bfloat16 *k_scale, *v_scale;
+  PageView pages;
+  const int32_t* cu_q;
+  int32_t batch, total_q, num_heads, kv_heads, group;
+  int64_t win_left, win_right;
+  float scale_log2;
+  unsigned int* err;
+  Span q_span, out_span, lse_span, kp_span, vp_span, ks_span, vs_span;  // bounds-checking build
+};
+
+struct PagedLaunch {
+  PagedParams p;
+  int head_dim, sms;
+  bool e4m3;
+};
+
+cudaError_t launch_paged(const PagedLaunch& L, cudaStream_t stream);
+
+}  // namespace varlen

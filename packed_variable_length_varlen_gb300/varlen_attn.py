@@ -41,6 +41,24 @@ class VarlenDenseStride(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
+class VarlenPageStride(ctypes.Structure):
+    """Page, row and head strides of one page array [num_pages, page_size, heads, D], in elements."""
+    _fields_ = [("page", ctypes.c_int64), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class VarlenKvCache(ctypes.Structure):
+    """varlen_kv_cache of the C header."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("seqlens", ctypes.c_void_p),
+                ("sk", VarlenPageStride), ("sv", VarlenPageStride), ("table_stride", ctypes.c_int64),
+                ("type", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+VARLEN_CACHE_BF16 = 0
+VARLEN_CACHE_E4M3 = 1
+
+
 class VarlenError(RuntimeError):
     def __init__(self, status: int, where: str):
         msg = "%s failed: %d (%s)" % (where, status, varlen_attn_status_string(status))
@@ -101,6 +119,14 @@ def _load() -> ctypes.CDLL:
     lib.varlen_attn_bwd_dense.restype = ctypes.c_int
     lib.varlen_attn_bwd_dense.argtypes = [vp, DS, vp, DS, vp, DS, vp, DS, vp, DS, vp, i32, i32, i32, i32, i32, f32,
                                           i32, vp, DS, vp, DS, vp, DS, vp, sz, vp]
+    lib.varlen_attn_cache_write.restype = ctypes.c_int
+    lib.varlen_attn_cache_write.argtypes = [vp, S, vp, S, vp, i32, i32, vp, vp]
+    lib.varlen_attn_cache_read.restype = ctypes.c_int
+    lib.varlen_attn_cache_read.argtypes = [vp, vp, i32, i32, vp, S, vp, S, vp]
+    lib.varlen_attn_fwd_paged_workspace_size.restype = sz
+    lib.varlen_attn_fwd_paged_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    lib.varlen_attn_fwd_paged.restype = ctypes.c_int
+    lib.varlen_attn_fwd_paged.argtypes = [vp, S, vp, i32, i32, i32, i32, vp, f32, i32, i32, vp, S, vp, vp, sz, vp]
     lib.varlen_attn_bwd_noalloc.restype = ctypes.c_int
     lib.varlen_attn_bwd_noalloc.argtypes = [vp, S, vp, S, vp, S, vp, S, vp, S, vp, vp, vp, i32, i32, i32, i32, i32,
                                             i32, i32, f32, vp, S, vp, S, vp, S, vp]
@@ -148,7 +174,8 @@ EXPORTED = ("varlen_attn_fwd", "varlen_attn_bwd_workspace_size", "varlen_attn_bw
             "varlen_attn_fwd_fp8_workspace_layout", "varlen_attn_fwd_fp8", "varlen_attn_bwd_noalloc_scratch_bytes",
             "varlen_attn_debug_noalloc_scratch", "varlen_attn_bounds_checked", "varlen_attn_debug_set_span_slack",
             "varlen_attn_debug_skip_load", "varlen_attn_debug_mma_cycles", "varlen_attn_fwd_fp8_window",
-            "varlen_attn_fwd_fp8_dense_workspace_size", "varlen_attn_fwd_fp8_dense")
+            "varlen_attn_fwd_fp8_dense_workspace_size", "varlen_attn_fwd_fp8_dense", "varlen_attn_cache_write",
+            "varlen_attn_cache_read", "varlen_attn_fwd_paged_workspace_size", "varlen_attn_fwd_paged")
 
 # Size of the fixed device array varlen_attn_bwd_noalloc uses as scratch, as
 # compiled into the library.
@@ -175,6 +202,10 @@ def _dstride(t) -> VarlenDenseStride:
     if t.dim() != 4 or t.stride(3) != 1:
         raise ValueError("dense tensors must be [batch, seqlen, heads, head_dim] with unit innermost stride")
     return VarlenDenseStride(t.stride(0), t.stride(1), t.stride(2))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
 
 
 def _stream(stream):
@@ -343,6 +374,28 @@ def varlen_attn_bwd_noalloc(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_k,
                                        _ptr(cu_seqlens_k), batch, total_q, total_k, num_heads, head_dim,
                                        max_seqlen_q, max_seqlen_k, scale, _ptr(dq), _stride(dq), _ptr(dk),
                                        _stride(dk), _ptr(dv), _stride(dv), _stream(stream))
+
+
+def varlen_attn_cache_write(k, v, cu_seqlens, batch, total, cache, stream=None) -> int:
+    """cache: a VarlenKvCache (PagedCache.struct), or None."""
+    return LIB.varlen_attn_cache_write(_ptr(k), _stride(k), _ptr(v), _stride(v), _ptr(cu_seqlens), batch, total,
+                                       _ref(cache), _stream(stream))
+
+
+def varlen_attn_cache_read(cache, cu_seqlens, batch, total, k, v, stream=None) -> int:
+    return LIB.varlen_attn_cache_read(_ref(cache), _ptr(cu_seqlens), batch, total, _ptr(k), _stride(k), _ptr(v),
+                                      _stride(v), _stream(stream))
+
+
+def varlen_attn_fwd_paged_workspace_size(batch, total_q, num_heads, num_kv_heads, head_dim) -> int:
+    return int(LIB.varlen_attn_fwd_paged_workspace_size(batch, total_q, num_heads, num_kv_heads, head_dim))
+
+
+def varlen_attn_fwd_paged(q, cu_seqlens_q, batch, total_q, num_heads, max_seqlen_q, cache, scale, window_left,
+                          window_right, out, lse, workspace, workspace_bytes, stream=None) -> int:
+    return LIB.varlen_attn_fwd_paged(_ptr(q), _stride(q), _ptr(cu_seqlens_q), batch, total_q, num_heads,
+                                     max_seqlen_q, _ref(cache), scale, window_left, window_right, _ptr(out),
+                                     _stride(out), _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream))
 
 
 def varlen_attn_debug_noalloc_scratch():
@@ -534,3 +587,148 @@ def attention_bwd_dense(q, k, v, out, dout, lse, scale=None, causal=False, dq=No
     _check(varlen_attn_bwd_dense(q, k, v, out, dout, lse, B, Sq, Sk, H, D, scale, causal, dq, dk, dv, workspace,
                                  workspace.numel(), stream), "varlen_attn_bwd_dense")
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------- paged cache
+
+class PagedCache:
+    """A paged key/value cache: the tensors a program keeps, checked once.
+
+    k_pages / v_pages  [num_pages, page_size, num_kv_heads, D], bf16 or
+                       float8_e4m3fn, unit innermost stride
+    block_table        [batch, max_pages] int32: page of each page_size positions
+    seqlens            [batch] int32: positions each sequence holds
+    k_scale / v_scale  E4M3 only: bf16 [num_pages, num_kv_heads, page_size],
+                       contiguous
+
+    The tensors are kept, not copied: what a program writes into them (a new
+    page in the table, longer seqlens) is seen by later calls.  ``struct`` is
+    the C description of them.
+    """
+
+    def __init__(self, k_pages, v_pages, block_table, seqlens, k_scale=None, v_scale=None):
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+            raise ValueError("k_pages and v_pages must be [num_pages, page_size, heads, head_dim] of one type")
+        if k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
+            raise ValueError("pages must have a unit innermost stride")
+        if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError("pages must be bfloat16 or float8_e4m3fn")
+        e4m3 = k_pages.dtype == torch.float8_e4m3fn
+        pages, page_size, heads, dim = k_pages.shape
+        if block_table.dim() != 2 or block_table.dtype != torch.int32 or (block_table.shape[1] > 1
+                                                                          and block_table.stride(1) != 1):
+            raise ValueError("block_table must be int32 [batch, max_pages] with unit innermost stride")
+        if seqlens.dtype != torch.int32 or seqlens.dim() != 1 or not seqlens.is_contiguous() \
+                or seqlens.shape[0] != block_table.shape[0]:
+            raise ValueError("seqlens must be contiguous int32 [batch]")
+        for s in (k_scale, v_scale):
+            if (s is not None) != e4m3:
+                raise ValueError("E4M3 pages need k_scale and v_scale, bf16 pages take none")
+            if e4m3 and (s.dtype != torch.bfloat16 or tuple(s.shape) != (pages, heads, page_size)
+                         or not s.is_contiguous()):
+                raise ValueError("scales must be contiguous bfloat16 [num_pages, heads, page_size]")
+        self.tensors = [t for t in (k_pages, v_pages, block_table, seqlens, k_scale, v_scale) if t is not None]
+        if any(t.device != k_pages.device for t in self.tensors):
+            raise ValueError("the cache's tensors must be on one device")
+        self.k_pages, self.v_pages, self.block_table, self.seqlens = k_pages, v_pages, block_table, seqlens
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.device, self.batch, self.num_kv_heads, self.head_dim = k_pages.device, seqlens.shape[0], heads, dim
+        c = VarlenKvCache()
+        c.k, c.v, c.block_table, c.seqlens = (t.data_ptr() for t in (k_pages, v_pages, block_table, seqlens))
+        if e4m3:
+            c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+        c.sk, c.sv = VarlenPageStride(*k_pages.stride()[:3]), VarlenPageStride(*v_pages.stride()[:3])
+        c.table_stride = block_table.stride(0)
+        c.type = VARLEN_CACHE_E4M3 if e4m3 else VARLEN_CACHE_BF16
+        c.num_pages, c.page_size, c.num_kv_heads, c.head_dim = pages, page_size, heads, dim
+        c.max_pages = block_table.shape[1]
+        self.struct = c
+
+
+def _check_packed(cache, cu_seqlens, *tensors):
+    """Types and places that the C entry points cannot see."""
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() \
+            or cu_seqlens.shape[0] != cache.batch + 1:
+        raise ValueError("cu_seqlens must be contiguous int32 [batch + 1]")
+    for t in (cu_seqlens,) + tensors:
+        if t.device != cache.device:
+            raise ValueError("every tensor must be on the cache's device")
+    for t in tensors:
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != cache.head_dim or t.stride(2) != 1:
+            raise ValueError("packed rows must be bfloat16 [rows, heads, head_dim] with unit innermost stride")
+
+
+def _launch(cache, stream, call, where, *fresh):
+    """Runs call(stream) with the cache's device current; tensors allocated
+    for the call (`fresh`) are kept from reuse until `stream` is done."""
+    if cache.device.type != "cuda":
+        raise ValueError("the cache must be on a CUDA device")
+    if cache.device.index is not None and cache.device.index != torch.cuda.current_device():
+        with torch.cuda.device(cache.device):
+            return _launch(cache, stream, call, where, *fresh)
+    if stream is not None:
+        own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        for t in fresh:
+            t.record_stream(own)
+    _check(call(stream), where)
+
+
+def cache_write(cache, k, v, cu_seqlens, stream=None):
+    """Writes packed new rows k, v ([rows, num_kv_heads, D] bf16) into the
+    cache: the rows of segment b become the last ones of its seqlens[b]
+    positions (seqlens already counts them)."""
+    _check_packed(cache, cu_seqlens, k, v)
+    if k.shape != v.shape or k.shape[1] != cache.num_kv_heads:
+        raise ValueError("k and v must be [rows, num_kv_heads, head_dim]")
+    _launch(cache, stream, lambda s: varlen_attn_cache_write(k, v, cu_seqlens, cache.batch, k.shape[0], cache.struct,
+                                                             s), "varlen_attn_cache_write")
+
+
+def cache_read(cache, cu_seqlens, total, k=None, v=None, stream=None):
+    """The last rows of every sequence, packed by cu_seqlens into bf16 k, v
+    ([total, num_kv_heads, D], allocated when None); returns (k, v)."""
+    fresh = []
+    if k is None:
+        k = torch.empty(total, cache.num_kv_heads, cache.head_dim, dtype=torch.bfloat16, device=cache.device)
+        fresh.append(k)
+    if v is None:
+        v = torch.empty(total, cache.num_kv_heads, cache.head_dim, dtype=torch.bfloat16, device=cache.device)
+        fresh.append(v)
+    _check_packed(cache, cu_seqlens, k, v)
+    if tuple(k.shape[:2]) != (total, cache.num_kv_heads) or k.shape != v.shape:
+        raise ValueError("k and v must be [total, num_kv_heads, head_dim]")
+    _launch(cache, stream, lambda s: varlen_attn_cache_read(cache.struct, cu_seqlens, cache.batch, total, k, v, s),
+            "varlen_attn_cache_read", *fresh)
+    return k, v
+
+
+def attention_fwd_paged(q, cache, cu_seqlens_q, max_seqlen_q=0, scale=None, out=None, lse=None, workspace=None,
+                        stream=None, causal=False, window=(-1, -1)):
+    """O and LSE of packed queries ([rows, H, D] bf16, H a multiple of the
+    cache's heads) over the cache, the last query of a segment at its
+    sequence's last position; `causal` / `window` as in attention_fwd.
+    max_seqlen_q, where known, lets short calls run on fewer kernels."""
+    _check_packed(cache, cu_seqlens_q, q)
+    total_q, H, D = q.shape
+    scale = float(D ** -0.5) if scale is None else float(scale)
+    fresh = []
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        fresh.append(out)
+    if lse is None:
+        lse = torch.empty(H, total_q, dtype=torch.float32, device=q.device)
+        fresh.append(lse)
+    if workspace is None:
+        nbytes = varlen_attn_fwd_paged_workspace_size(cache.batch, total_q, H, cache.num_kv_heads, D)
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        fresh.append(workspace)
+    _check_packed(cache, cu_seqlens_q, out)
+    if out.shape != q.shape or lse.dtype != torch.float32 or tuple(lse.shape) != (H, total_q) \
+            or not lse.is_contiguous() or lse.device != q.device or workspace.device != q.device:
+        raise ValueError("out must have q's shape, lse be contiguous float32 [H, rows], all on q's device")
+    left, right = _band(causal, window) or (-1, -1)
+    _launch(cache, stream, lambda s: varlen_attn_fwd_paged(q, cu_seqlens_q, cache.batch, total_q, H, max_seqlen_q,
+                                                           cache.struct, scale, left, right, out, lse, workspace,
+                                                           workspace.numel() * workspace.element_size(), s),
+            "varlen_attn_fwd_paged", *fresh)
+    return out, lse

@@ -341,7 +341,8 @@ int varlen_attn_fwd_fp8_dense(const void* q, varlen_dense_stride sq, const void*
  * must not overlap (ordering the dimensions of extent > 1 by stride, the
  * smallest is at least head_dim and each further one at least the previous
  * extent times the previous stride; VARLEN_ERR_STRIDE).  page_size is a power
- * of two from 16 to 1024, num_pages >= 1, max_pages * page_size < 2^31.  The
+ * of two from 16 to 1024, num_pages >= 1, max_pages * page_size <= 2^31 - 2048.
+ * The
  * struct itself is host memory, read during the call only.
  */
 enum { VARLEN_CACHE_BF16 = 0, VARLEN_CACHE_E4M3 = 1 };

@@ -103,12 +103,75 @@ struct PagedParams {
   Span q_span, out_span, lse_span, kp_span, vp_span, ks_span, vs_span;  // bounds-checking build
 };
 
+// What a kernel takes: segments of at most kFewRows rows, of more, or all.
+enum PagedTake : int32_t { kTakeFew = 0, kTakeMany = 1, kTakeAll = 2 };
+
+constexpr int kFewRows = 64;      // rows (queries x heads of a group) of a unit of the kernel for few rows
+constexpr int kFewTile = 64;      // keys per tile of that kernel
+constexpr int kFewCtasPerSm = 2;
+constexpr int kMaxSms = 160;      // the workspace is sized for this many
+
+// What CTA c left for the join: the unit that it begins and does not end, and
+// the number of CTAs that hold it (0: none).
+struct PagedJoin {
+  int32_t b, kh, blk, parts;
+};
+
+// Partial results of one kernel in the workspace: slot 2 c + (the CTA begins
+// the unit) holds rows [rows][D] of the unnormalised output and [rows][2] of
+// (m, l), m in the exp2 domain.
+struct PagedParts {
+  float* o;
+  float* ml;
+  PagedJoin* join;
+  int32_t rows;
+};
+
 struct PagedLaunch {
   PagedParams p;
   int head_dim, sms;
-  bool e4m3;
+  bool e4m3, few_only;
+  CUtensorMap few_k, few_v, few_ks, few_vs;  // pages and (E4M3) scales in boxes of up to kFewTile keys
+  PagedParts few;
 };
 
+// Byte offsets of the workspace.
+struct PagedWorkspace {
+  size_t few_o, few_ml, few_join, bytes;
+  int32_t few_rows;
+};
+inline PagedWorkspace paged_workspace(int64_t total_rows, int32_t head_dim) {
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  PagedWorkspace w;
+  w.few_rows = (int32_t)(total_rows < kFewRows ? (total_rows < 1 ? 1 : total_rows) : kFewRows);
+  const size_t ctas = (size_t)kFewCtasPerSm * kMaxSms;
+  w.few_o = 0;
+  w.few_ml = up(w.few_o + 2 * ctas * w.few_rows * head_dim * 4);
+  w.few_join = up(w.few_ml + 2 * ctas * w.few_rows * 8);
+  w.bytes = up(w.few_join + ctas * sizeof(PagedJoin));
+  return w;
+}
+
+// A kernel whose launch may begin while the one before it on the stream ends;
+// it waits (dependency_wait) before it touches memory.
+template <class... P, class... A>
+cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                              const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
+cudaError_t launch_paged_few(const PagedLaunch& L, int32_t take, cudaStream_t stream);
+cudaError_t launch_paged_join(const PagedLaunch& L, cudaStream_t stream);
 cudaError_t launch_paged(const PagedLaunch& L, cudaStream_t stream);
 
 }  // namespace varlen

@@ -1,7 +1,7 @@
 // varlen_paged_api.cu -- the C entry points of the paged cache and of the
 // attention over it (declared in varlen_attn.h): argument checks, 64-bit
 // extents, launches.
-#include <climits>
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <utility>
@@ -52,7 +52,7 @@ int check_cache(const varlen_kv_cache* cache, int32_t batch, int* page_shift) {
   int shift = 4;
   while (shift < 11 && (1 << shift) != c.page_size) ++shift;
   if (shift == 11) return VARLEN_ERR_SHAPE;
-  if (((int64_t)c.max_pages << shift) > INT32_MAX) return VARLEN_ERR_SHAPE;
+  if (((int64_t)c.max_pages << shift) > (int64_t(1) << 31) - 2048) return VARLEN_ERR_SHAPE;  // tile ends stay in int32
   if (c.head_dim != 64 && c.head_dim != 96 && c.head_dim != 128) return VARLEN_ERR_HEAD_DIM;
   if (c.k == nullptr || c.v == nullptr || c.seqlens == nullptr || (c.max_pages > 0 && c.block_table == nullptr))
     return VARLEN_ERR_NULL;
@@ -68,6 +68,28 @@ int check_cache(const varlen_kv_cache* cache, int32_t batch, int* page_shift) {
 
 PageView view_of(const varlen_kv_cache& c, int shift) {
   return PageView{c.block_table, c.table_stride, c.seqlens, c.num_pages, c.max_pages, c.page_size, shift};
+}
+
+// Pages as {D, heads, page rows, pages} in boxes of 128 bytes (64 bf16 or 128
+// codes, zero past D) of `rows` rows of one head and page.
+int encode_pages(CUtensorMap* map, const varlen_kv_cache& c, const void* base, varlen_page_stride s, int rows) {
+  const cuuint64_t es = (cuuint64_t)elem_bytes(c), D = (cuuint64_t)c.head_dim;
+  // (a stride over one element is never used: a legal value for it)
+  const cuuint64_t head = c.num_kv_heads > 1 ? s.head * es : D * es, page = c.num_pages > 1 ? s.page * es : D * es;
+  const cuuint64_t dims[4] = {D, (cuuint64_t)c.num_kv_heads, (cuuint64_t)c.page_size, (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[3] = {head, s.row * es, page};
+  const cuuint32_t box[4] = {(cuuint32_t)(128 / es), 1u, (cuuint32_t)rows, 1u};
+  return encode_tiled(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims,
+                      strides, box, true);
+}
+
+// Scales as {page rows, heads, pages} in boxes of `rows` scales.
+int encode_scales(CUtensorMap* map, const varlen_kv_cache& c, const void* base, int rows) {
+  const cuuint64_t n = (cuuint64_t)c.page_size;
+  const cuuint64_t dims[3] = {n, (cuuint64_t)c.num_kv_heads, (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[2] = {n * 2, n * 2 * (cuuint64_t)c.num_kv_heads};
+  const cuuint32_t box[3] = {(cuuint32_t)rows, 1u, 1u};
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, false);
 }
 
 int cache_impl(const void* k, varlen_stride sk, const void* v, varlen_stride sv, const int32_t* cu, int32_t batch,
@@ -145,7 +167,7 @@ extern "C" int varlen_attn_cache_read(const varlen_kv_cache* cache, const int32_
 extern "C" size_t varlen_attn_fwd_paged_workspace_size(int32_t batch, int32_t total_q, int32_t num_heads,
                                                        int32_t num_kv_heads, int32_t head_dim) {
   if (batch < 0 || total_q < 0 || num_heads < 0 || num_kv_heads < 1 || head_dim < 0) return 0;
-  return 256;
+  return paged_workspace((int64_t)total_q * (num_heads / num_kv_heads), head_dim).bytes;
 }
 
 extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int32_t* cu_seqlens_q, int32_t batch,
@@ -153,7 +175,6 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
                                      const varlen_kv_cache* cache, float scale, int32_t window_left,
                                      int32_t window_right, void* out, varlen_stride so, float* lse, void* workspace,
                                      size_t workspace_bytes, void* stream) {
-  (void)max_seqlen_q;
   int shift = 0;
   int st = check_cache(cache, batch, &shift);
   if (st != VARLEN_OK) return st;
@@ -212,8 +233,21 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   p.ks_span = checked_span(c.k_scale, scale_bytes(c));
   p.vs_span = checked_span(c.v_scale, scale_bytes(c));
   L.head_dim = c.head_dim;
-  L.sms = sms;
+  L.sms = std::min(sms, kMaxSms);
   L.e4m3 = c.type == VARLEN_CACHE_E4M3;
+  L.few_only = (int64_t)total_q * p.group <= kFewRows ||
+               (max_seqlen_q > 0 && (int64_t)max_seqlen_q * p.group <= kFewRows);
+  char* ws = static_cast<char*>(workspace);
+  const PagedWorkspace w = paged_workspace((int64_t)total_q * p.group, c.head_dim);
+  L.few = PagedParts{reinterpret_cast<float*>(ws + w.few_o), reinterpret_cast<float*>(ws + w.few_ml),
+                     reinterpret_cast<PagedJoin*>(ws + w.few_join), w.few_rows};
+  const int box = std::min(c.page_size, kFewTile);
+  if ((st = encode_pages(&L.few_k, c, c.k, c.sk, box)) != VARLEN_OK) return st;
+  if ((st = encode_pages(&L.few_v, c, c.v, c.sv, box)) != VARLEN_OK) return st;
+  if (L.e4m3) {
+    if ((st = encode_scales(&L.few_ks, c, c.k_scale, box)) != VARLEN_OK) return st;
+    if ((st = encode_scales(&L.few_vs, c, c.v_scale, box)) != VARLEN_OK) return st;
+  }
   const cudaError_t e = launch_paged(L, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VARLEN_OK : cuda_fail(e);
 }

@@ -318,10 +318,12 @@ int encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const voi
                  const cuuint64_t* byte_strides, const cuuint32_t* box, bool swizzle) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return VARLEN_ERR_CUDA;
+  // rows of up to 128 bytes: fetching 256 would bring in bytes of other heads
+  const CUtensorMapL2promotion promote = CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
   cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
   CUresult r = enc(map, type, (cuuint32_t)rank, const_cast<void*>(base), dims, byte_strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? VARLEN_OK : VARLEN_ERR_STRIDE;
 }
 

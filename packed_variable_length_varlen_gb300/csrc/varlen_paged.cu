@@ -8,8 +8,6 @@ namespace varlen {
 
 namespace {
 
-using FewGeom = PagedGeom<kFewRows, kFewTile, false>;
-
 // One unit per CTA of the attention kernel that began but did not end one
 // (blockIdx.x; most have none), its rows shared out over blockIdx.y.  With
 // parts i in the order of the CTAs: m = max m_i, l = sum l_i 2^(m_i - m),
@@ -17,7 +15,7 @@ using FewGeom = PagedGeom<kFewRows, kFewTile, false>;
 // part, and their sums are added in the order of the warps.
 constexpr int kJoinWarps = 8, kJoinRows = 8;
 
-template <int D, class G>
+template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     varlen_paged_join_kernel(const PagedParams p, const PagedParts parts) {
   __shared__ float so[kJoinWarps][D], sm[kJoinWarps], sl[kJoinWarps];
@@ -74,7 +72,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 
 template <int D>
 cudaError_t launch_join_d(const PagedLaunch& L, cudaStream_t stream) {
-  return launch_overlapped(varlen_paged_join_kernel<D, FewGeom>, dim3(L.sms * kFewCtasPerSm, kJoinRows), kJoinWarps * 32,
+  return launch_overlapped(varlen_paged_join_kernel<D>, dim3(L.sms * kFewCtasPerSm, kJoinRows), kJoinWarps * 32,
                            0, stream, L.p, L.few);
 }
 

@@ -106,8 +106,9 @@ struct PagedParams {
 // What a kernel takes: segments of at most kFewRows rows, of more, or all.
 enum PagedTake : int32_t { kTakeFew = 0, kTakeMany = 1, kTakeAll = 2 };
 
-constexpr int kFewRows = 64;      // rows (queries x heads of a group) of a unit of the kernel for few rows
-constexpr int kFewTile = 64;      // keys per tile of that kernel
+constexpr int kFewRows = 32;      // rows (queries x heads of a group) of a unit of the kernel for few rows
+// keys per tile of that kernel: 16 KB of K at D = 128, in either type
+constexpr int few_tile(bool e4m3) { return e4m3 ? 128 : 64; }
 constexpr int kFewCtasPerSm = 2;
 constexpr int kMaxSms = 160;      // the workspace is sized for this many
 
@@ -131,7 +132,7 @@ struct PagedLaunch {
   PagedParams p;
   int head_dim, sms;
   bool e4m3, few_only;
-  CUtensorMap few_k, few_v, few_ks, few_vs;  // pages and (E4M3) scales in boxes of up to kFewTile keys
+  CUtensorMap few_k, few_v, few_ks, few_vs;  // pages and (E4M3) scales in boxes of up to few_tile keys
   PagedParts few;
 };
 

@@ -1,31 +1,44 @@
 // varlen_paged_few.cu -- attention over the paged cache for few query rows:
 // single tokens, drafted tokens, short chunks.
 //
-// Bound: every key and value is read once for at most 64 rows (query tokens
+// Bound: every key and value is read once for at most 32 rows (query tokens
 // times the query heads that share a key head), so the memory's rate decides
 // and the matrix products only have to keep up with it.  At 6.8 TB/s an SM
-// receives 44.7 bytes a nanosecond, 12 bf16 or 23 E4M3 elements a cycle; with
-// 16 rows the warp-level m16n8k16 products cost 16 multiply-adds an element,
-// a fraction of their rate, which is why they are used here and the
-// tcgen05 units, whose tiles have 128 rows, are not.
+// receives 44.7 bytes a nanosecond, 12 bf16 or 23 E4M3 elements a cycle.  The
+// warp-level m16n8k16 products take keys (then columns of V) as their 16 rows
+// and query rows as their 8 columns, S^T = K Q^T and O^T = V^T P^T: a step of 16
+// keys for 8 rows is 16 products at D = 128, and o takes 32 registers, so that
+// enough warps stay resident to hide the chain of products, softmax and
+// products.  (The other way round, 16 query rows by 8 keys, costs twice the
+// products and registers while most of the 16 rows are empty: 214 us where this
+// form takes FIGURE for 64 ragged E4M3 sequences.)
 //
-// A CTA is four consumer warps and a producer warp; two CTAs share an SM.
-// The producer streams 64-key tiles of K and of V, page piece by page piece,
-// through a ring of shared-memory slots by TMA (an entry that names no page,
-// and positions past the sequence, become an out-of-range page: zeros, no
-// traffic).  Rows are taken in tiles of 16: a unit of up to 16 rows splits each
-// tile's keys over the four warps, of up to 32 rows over two pairs, and 64 rows
-// give every warp its own rows and all keys.  Each warp runs its own online
-// softmax (m, l, o in registers, 32-bit); at the end of a unit the warps that
-// share rows join theirs through shared memory, in a fixed order.
+// A CTA is a few consumer warps and a producer warp; two CTAs share an SM.
+// The producer streams tiles of K and of V, page piece by page piece, through
+// a ring of shared-memory slots by TMA (an entry that names no page, and
+// positions past the sequence, become an out-of-range page: zeros, no
+// traffic).  Rows are taken in tiles of 8; the warps that share a row tile split
+// each key tile, every one with its own online softmax (m, l, o in registers,
+// 32-bit), and join theirs through shared memory at the end of a unit, in a
+// fixed order.
 //
-// Operands need no shuffling.  The product S = Q K^T sums over d, so both
-// operands may take d in any order: a lane reads 16 consecutive bytes of its
-// key's row, and Q is loaded to match.  The same holds for the columns of
-// O = P V: with E4M3 a lane reads D/8 consecutive bytes of each of its four
-// keys, which stand for its column of D/8 different n-tiles.  An E4M3 code s
-// eeee mmm becomes a bf16 by moving its bits to s 0000eeee mmm0000, which is
-// code * 2^-120 exactly (subnormals too), times 2^120 * scale.
+// Operands need no shuffling but for P, which is transposed in registers.  S
+// sums over d, so both operands may take d in any order: a lane reads 16
+// consecutive bytes of its key's row, and Q is loaded to match.  The same holds
+// for the order of O's columns: with E4M3 a lane reads D/8 consecutive bytes of
+// each of its four keys, which stand for its row of D/8 different half-tiles.
+//
+// E4M3 codes become f16 (exact, two a conversion) and both products run in
+// f16 with 32-bit sums.  What f16 lacks in range the scales make up for:
+//   S: a row of Q is multiplied by the power of two that brings its largest
+//      element to 2^14 (f16 then holds all of a bf16 that is not 2^-28 of the
+//      largest), and S by that power's inverse and the key's scale.
+//   P V: the weight of key j is P_j s_j / R * 2^7, with R the largest scale
+//      that the warp has met (o is kept in units of R 2^-7): at most 2^15, and
+//      f16's 11 bits hold down to 2^-21 of the largest term.  Where a key's
+//      scale lies more than 2^12 below R (or is NaN), the step's products run
+//      in bf16 instead: a code's bits s eeee mmm moved to s 0000eeee mmm0000 are
+//      the bf16 code * 2^-120, subnormals too, times 2^127 s / R.
 #include <cuda_fp8.h>
 
 #include "sm103_ptx.cuh"
@@ -36,37 +49,54 @@ namespace varlen {
 
 namespace {
 
-using FewGeom = PagedGeom<kFewRows, kFewTile, false>;
-
-constexpr int kWarps = 4;                         // consumer warps
-constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kLeastTiles = 2;                    // tiles per CTA when there are few
+constexpr int kLeastTiles = 2;  // tiles per CTA when there are few
+constexpr int kMaxSlots = 8;
 
 template <int D, bool E4M3>
 struct FewCfg {
+  static constexpr int WARPS = E4M3 ? 8 : 4;                // consumer warps
+  static constexpr int THREADS = (WARPS + 1) * 32;
+  static constexpr int KT = few_tile(E4M3);                 // keys per tile
+  static constexpr int STEP = 16;                           // keys a warp takes at a time
+  using Geom = PagedGeom<kFewRows, KT, false>;
   static constexpr int CK = E4M3 ? 1 : (D + 63) / 64;       // 128-byte column chunks of a row
-  static constexpr int CHUNK = kFewTile * 128;
+  static constexpr int CHUNK = KT * 128;
   static constexpr int TILE = CK * CHUNK;
-  static constexpr int SCALES = E4M3 ? 512 : 0;             // up to four page pieces, 128 bytes apart
-  static constexpr int NSLOT = E4M3 ? 8 : (CK == 1 ? 8 : 5);
+  static constexpr int SCALES = E4M3 ? KT * 8 : 0;          // page pieces of at least 16 keys, 128 bytes apart
+  static constexpr int NSLOT = !E4M3 && CK == 1 ? 8 : 5;
   static constexpr int KSTEPS = E4M3 ? (D == 64 ? 4 : 8) : CK * 4;
-  static constexpr int NT = D / 8;                          // n-tiles of O
-  static constexpr int XCHG = (NT * 4 + 4) * 32 * 4;        // one warp's (o, m, l)
-  static constexpr int SMEM = 1024 + NSLOT * (TILE + SCALES) + 2 * XCHG;
+  static constexpr int MT = D / 16;                         // m-tiles of O^T
+  static constexpr int XCHG = (MT * 4 + 4) * 32 * 4;        // one warp's (o, m, l)
+  static constexpr int SMEM = 1024 + NSLOT * (TILE + SCALES) + WARPS / 2 * XCHG;
 };
 
 struct FewShared {
-  uint64_t full[8], empty[8], join;
+  uint64_t full[kMaxSlots], empty[kMaxSlots], join;
   int abort;
   PagedStart start;
 };
 static_assert(sizeof(FewShared) <= 1024, "barrier block too large");
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// d += A B: A 16 x 16 (a: rows r, r + 8 of its first eight columns, then of its
+// last), B 16 x 8 (b), bf16 or f16 with 32-bit sums.
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit elements, two a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
@@ -76,20 +106,9 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
+template <class T>
+__device__ __forceinline__ T lds(const uint8_t* p) {
+  return *reinterpret_cast<const T*>(p);
 }
 
 // Byte offset of bytes [off, ...) of row `row` in a tile of 128-byte rows
@@ -105,20 +124,19 @@ __device__ __forceinline__ uint32_t mul_pair(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
-// 2^120 * scale as two bf16 factors: f, and a rest that is 1 unless the
-// product passes 2^127 (a scale above 2^7).
-struct Factor {
-  uint32_t f, rest;  // pairs
-};
-__device__ __forceinline__ Factor factor_of(uint32_t scales) {  // two bf16 scales
-  const float a = __uint_as_float(scales << 16) * 0x1p120f, b = __uint_as_float(scales & 0xffff0000u) * 0x1p120f;
-  const bool la = a > 0x1p127f, lb = b > 0x1p127f;
-  Factor x;
-  x.f = pack_bf16x2(la ? 0x1p127f : a, lb ? 0x1p127f : b);
-  x.rest = pack_bf16x2(la ? __uint_as_float(scales << 16) * 0x1p-7f : 1.f,
-                       lb ? __uint_as_float(scales & 0xffff0000u) * 0x1p-7f : 1.f);
-  return x;
+// Two codes (the low 16 bits of w) as f16.
+__device__ __forceinline__ uint32_t f16_pair(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(w));
+  return h;
 }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+  return h;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // Shared-memory offset of the scale of key r of a tile whose page pieces hold
 // 1 << shift keys.
@@ -127,7 +145,7 @@ __device__ __forceinline__ uint32_t scale_at(uint32_t r, int shift) {
 }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads, kFewCtasPerSm)
+__global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, kFewCtasPerSm)
     varlen_paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                             const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
                             const PagedParams p, const PagedParts parts, int32_t take) {
@@ -146,27 +164,27 @@ __global__ void __launch_bounds__(kThreads, kFewCtasPerSm)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NSLOT; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], kWarps);
+      mbar_init(&sh.empty[i], C::WARPS);
     }
-    mbar_init(&sh.join, kWarps * 32);
+    mbar_init(&sh.join, C::WARPS * 32);
     sh.abort = 0;
     fence_barrier_init();
   }
   dependency_wait();  // nothing above reads or writes global memory
-  paged_start<FewGeom>(sh.start, p, take, kLeastTiles);
+  paged_start<typename C::Geom>(sh.start, p, take, kLeastTiles);
   dependents_may_launch();
-  PagedWalk<FewGeom> walk;
+  PagedWalk<typename C::Geom> walk;
   PagedPiece x;
-  const int box_shift = min(p.pages.page_shift, 6);  // keys of one page piece of a tile
+  const int box_shift = min(p.pages.page_shift, E4M3 ? 7 : 6);  // keys of one page piece of a tile
 
-  if (warp == kWarps) {
+  if (warp == C::WARPS) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       parts.join[blockIdx.x].parts = 0;
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
-    const int pieces = kFewTile >> box_shift;
+    const int pieces = C::KT >> box_shift;
     const bool loads = lane < pieces * C::CK, loads_scale = E4M3 && lane < pieces;
     const int piece = lane % pieces, cc = lane / pieces;
     uint32_t pos = 0;
@@ -176,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, kFewCtasPerSm)
       if (lane == 0) paged_note(parts.join, sh.start, x);
       const int32_t tiles = min(x.j1, x.u.tiles);
       for (int32_t j = x.j0; ok && j < tiles; ++j) {
-        const int32_t key = (x.u.tile0 + j) * kFewTile + (piece << box_shift);
+        const int32_t key = (x.u.tile0 + j) * C::KT + (piece << box_shift);
         int32_t page = p.pages.num_pages;
         if (loads && key < x.u.hi && key + (1 << box_shift) > x.u.lo)
           page = page_at(p.pages, x.b, key >> p.pages.page_shift, p.err);
@@ -188,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, kFewCtasPerSm)
             ok = false;
             break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], C::TILE + (E4M3 ? kFewTile * 2 : 0));
+          if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], C::TILE + (E4M3 ? C::KT * 2 : 0));
           __syncwarp();
           if (loads)
             tma_load_4d(ring + slot * C::TILE + cc * C::CHUNK + ((piece << box_shift) * 128), which ? &tm_v : &tm_k,
@@ -215,63 +233,62 @@ __global__ void __launch_bounds__(kThreads, kFewCtasPerSm)
     bool ok = true;
     walk.init(sh.start, p, take);
     while (ok && walk.next(p, x)) {
-      const int32_t rows = (int32_t)min((int64_t)x.n * p.group - (int64_t)x.blk * kFewRows, (int64_t)kFewRows);
-      const int mt = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);  // row tiles; kWarps / mt warps share each
-      const int rt = warp & (mt - 1), kg = warp / mt, share = kWarps / mt;
-      const bool works = rt * 16 < rows;
-      // this lane's two rows
-      int32_t tok[2], hd[2];
-      bool live[2];
-      int32_t klo[2], khi[2];
+      // rows of the unit: first is row `skip` of token t0
+      const int32_t skip = (int32_t)((int64_t)x.blk * kFewRows - (int64_t)x.u.t0 * p.group);
+      const int32_t rows = min((x.n - x.u.t0) * (int64_t)p.group - skip, (int64_t)kFewRows);
+      const int mt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);  // row tiles
+      const int rt = warp & (mt - 1), kg = warp / mt, share = C::WARPS / mt;
+      const bool works = rt * 8 < rows;
+      // the operand B holds row r of the tile; the sums hold rows 2c, 2c + 1
+      int32_t tok[2], klo[2], khi[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int32_t rr = rt * 16 + r + i * 8;
-        live[i] = rr < rows;
-        const int64_t row = (int64_t)x.blk * kFewRows + min(rr, rows - 1);
-        tok[i] = (int32_t)(row / p.group);
-        hd[i] = x.kh * p.group + (int32_t)(row - (int64_t)tok[i] * p.group);
+        tok[i] = x.u.t0 + (skip + min(rt * 8 + 2 * c + i, rows - 1)) / p.group;
         band_keys(tok[i], tok[i], x.n, x.sk, p.win_left, p.win_right, &klo[i], &khi[i]);
       }
-      uint32_t qf[C::KSTEPS][4];
+      uint32_t qf[C::KSTEPS][2];
+      float rowf[2] = {p.scale_log2, p.scale_log2};
       if (works) {
+        const bool live = rt * 8 + r < rows;
+        const int32_t at = skip + min(rt * 8 + r, rows - 1), t = at / p.group;
+        const __nv_bfloat16* qa =
+            p.q + (int64_t)(x.q0 + x.u.t0 + t) * p.q_rs + (int64_t)(x.kh * p.group + at - t * p.group) * p.q_hs;
+        auto load = [&](int d0) {
+          return live && d0 < D && in_span(p.q_span, qa + d0, 16, p.err) ? __ldg(reinterpret_cast<const uint4*>(qa + d0))
+                                                                        : make_uint4(0, 0, 0, 0);
+        };
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const __nv_bfloat16* qa = p.q + (int64_t)(x.q0 + tok[i]) * p.q_rs + (int64_t)hd[i] * p.q_hs;
-          if constexpr (E4M3) {
+        for (int s = 0; s < C::KSTEPS / 2; ++s) {  // eight elements of this lane
+          const uint4 u = load(E4M3 ? (C::KSTEPS == 4 ? c : 2 * c + (s >> 1)) * 16 + (s & 1) * 8
+                                    : (s >> 1) * 64 + (2 * c + (s & 1)) * 8);
+          qf[2 * s][0] = u.x;
+          qf[2 * s][1] = u.y;
+          qf[2 * s + 1][0] = u.z;
+          qf[2 * s + 1][1] = u.w;
+        }
+        if constexpr (E4M3) {  // to f16, the row's largest element at 2^14
+          uint32_t top = 0;
 #pragma unroll
-            for (int s = 0; s < C::KSTEPS / 4; ++s) {
-              const int d0 = (C::KSTEPS == 4 ? c : 2 * c + s) * 16;  // 16 elements of this lane
-              uint4 u[2];
+          for (int k = 0; k < C::KSTEPS; ++k)
+            top = __vmaxu2(top, __vmaxu2(qf[k][0] & 0x7fff7fffu, qf[k][1] & 0x7fff7fffu));
+          top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // its biased exponent, within what leaves both powers normal
+          const int e = min(max((int)(max(top & 0xffffu, top >> 16) >> 7), 15), 254);
+          const float up = __uint_as_float((uint32_t)(254 + 14 - e) << 23);
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
-                u[k] = live[i] && d0 < D && in_span(p.q_span, qa + d0 + k * 8, 16, p.err)
-                           ? __ldg(reinterpret_cast<const uint4*>(qa + d0 + k * 8))
-                           : make_uint4(0, 0, 0, 0);
-              const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+          for (int k = 0; k < C::KSTEPS; ++k)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {  // elements 1, 3 then 0, 2 of each four
-                qf[s * 4 + k][i] = __byte_perm(w[2 * k], w[2 * k + 1], 0x7632);
-                qf[s * 4 + k][2 + i] = __byte_perm(w[2 * k], w[2 * k + 1], 0x5410);
-              }
-            }
-          } else {
+            for (int y = 0; y < 2; ++y) qf[k][y] = pack_f16x2(bf16_lo(qf[k][y]) * up, bf16_hi(qf[k][y]) * up);
 #pragma unroll
-            for (int s = 0; s < C::KSTEPS / 2; ++s) {
-              const int d0 = (s >> 1) * 64 + (2 * c + (s & 1)) * 8;
-              const uint4 u = live[i] && d0 < D && in_span(p.q_span, qa + d0, 16, p.err)
-                                  ? __ldg(reinterpret_cast<const uint4*>(qa + d0))
-                                  : make_uint4(0, 0, 0, 0);
-              qf[s * 2][i] = u.x;
-              qf[s * 2][2 + i] = u.y;
-              qf[s * 2 + 1][i] = u.z;
-              qf[s * 2 + 1][2 + i] = u.w;
-            }
-          }
+          for (int i = 0; i < 2; ++i)
+            rowf[i] *= __uint_as_float((uint32_t)(__shfl_sync(0xffffffffu, e, (2 * c + i) * 4) - 14) << 23);
         }
       }
-      float o[C::NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      float vref = 0.f, vinv = 0.f;  // E4M3: R and 2^7 / R
+      float o[C::MT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-      for (int t = 0; t < C::NT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+      for (int t = 0; t < C::MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
       // keys that every row of the unit sees: no select needed
       int32_t all_lo, all_hi;
       {
@@ -287,82 +304,74 @@ __global__ void __launch_bounds__(kThreads, kFewCtasPerSm)
           break;
         }
         __syncwarp();
-        const uint32_t kt = smem_addr(ring + ks * C::TILE), vt = smem_addr(ring + vs * C::TILE);
-        const uint32_t ksc = smem_addr(scales + ks * C::SCALES), vsc = smem_addr(scales + vs * C::SCALES);
-        const int32_t key0 = (x.u.tile0 + j) * kFewTile;
-        const bool edge = key0 < all_lo || key0 + kFewTile > all_hi;
+        const uint8_t *kt = ring + ks * C::TILE, *vt = ring + vs * C::TILE;
+        const uint8_t *ksc = scales + ks * C::SCALES, *vsc = scales + vs * C::SCALES;
+        const int32_t key0 = (x.u.tile0 + j) * C::KT;
+        const bool edge = key0 < all_lo || key0 + C::KT > all_hi;
         // rows of V that no row of the unit sees may hold anything: cleared
-        const bool vedge = key0 < x.u.lo || key0 + kFewTile > x.u.hi;
+        const bool vedge = key0 < x.u.lo || key0 + C::KT > x.u.hi;
         bool v_here = false;
-        // the 16-key steps of this warp: kg, kg + share, ...
+        // the steps of this warp: kg, kg + share, ...
 #pragma unroll 1
-        for (int a = kg * 16; a < kFewTile; a += share * 16) {
-          float s[2][4];
+        for (int a = kg * C::STEP; a < C::KT; a += share * C::STEP) {
+          float s[4], s2[4];  // keys a + r and a + r + 8 of rows 2c, 2c + 1; s2: a second chain of products
           if (works) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
-              const uint32_t row = a + h * 8 + r;
+            for (int e = 0; e < 4; ++e) s[e] = s2[e] = 0.f;
+            constexpr int NL = E4M3 ? C::KSTEPS / 4 : C::KSTEPS / 2;  // 16-byte loads of a key
+            uint4 u[NL], v[NL];
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+              const uint32_t at = E4M3 ? swz(a + r, (C::KSTEPS == 4 ? c : 2 * c + i) * 16)
+                                       : (i >> 1) * C::CHUNK + swz(a + r, (2 * c + (i & 1)) * 16);
+              u[i] = lds<uint4>(kt + at);
+              v[i] = lds<uint4>(kt + at + 8 * 128);  // eight rows on: the same place in the swizzle
+            }
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
               if constexpr (E4M3) {
-                uint32_t sc;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc) : "r"(ksc + scale_at(row, box_shift)) : "memory");
-                const Factor f = factor_of(sc | (sc << 16));
-                const bool rest = __any_sync(0xffffffffu, f.rest != 0x3f803f80u);
+                const uint32_t x0[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, x1[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-                for (int i = 0; i < C::KSTEPS / 4; ++i) {
-                  const uint4 u = lds128(kt + swz(row, (C::KSTEPS == 4 ? c : 2 * c + i) * 16));
-                  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    uint32_t b0 = mul_pair(raw_pair(w[k]), f.f);
-                    uint32_t b1 = mul_pair(raw_pair(w[k] << 8), f.f);
-                    if (rest) {
-                      b0 = mul_pair(b0, f.rest);
-                      b1 = mul_pair(b1, f.rest);
-                    }
-                    mma16816(s[h], qf[i * 4 + k], b0, b1);
-                  }
-                }
+                for (int k = 0; k < 4; ++k)
+                  mma16816<true>((k & 1) ? s2 : s, f16_pair(x0[k]), f16_pair(x1[k]), f16_pair(x0[k] >> 16),
+                                 f16_pair(x1[k] >> 16), qf[i * 4 + k][0], qf[i * 4 + k][1]);
               } else {
-#pragma unroll
-                for (int i = 0; i < C::KSTEPS / 2; ++i) {
-                  const uint4 u = lds128(kt + (i >> 1) * C::CHUNK + swz(row, (2 * c + (i & 1)) * 16));
-                  mma16816(s[h], qf[2 * i], u.x, u.y);
-                  mma16816(s[h], qf[2 * i + 1], u.z, u.w);
-                }
+                mma16816<false>(s, u[i].x, v[i].x, u[i].y, v[i].y, qf[2 * i][0], qf[2 * i][1]);
+                mma16816<false>(s2, u[i].z, v[i].z, u[i].w, v[i].w, qf[2 * i + 1][0], qf[2 * i + 1][1]);
               }
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = (s[e] + s2[e]) * rowf[e & 1];
+            if constexpr (E4M3) {
+              const float k0 = __bfloat162float(lds<__nv_bfloat16>(ksc + scale_at(a + r, box_shift)));
+              const float k1 = __bfloat162float(lds<__nv_bfloat16>(ksc + scale_at(a + r + 8, box_shift)));
+              s[0] *= k0;
+              s[1] *= k0;
+              s[2] *= k1;
+              s[3] *= k1;
+            }
           }
-          if (a + share * 16 >= kFewTile) {  // the warp's last step on this K tile
+          if (a + share * C::STEP >= C::KT) {  // the warp's last step on this K tile
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.empty[ks]);
           }
-          uint32_t pf[4];
           if (works) {
-            // columns of this lane: keys a + h*8 + 2c, +1
-            float mx[2] = {-INFINITY, -INFINITY}, sub[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
+            if (edge) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                float v = s[h][e] * p.scale_log2;
-                if (edge) {
-                  const int32_t key = key0 + a + h * 8 + 2 * c + (e & 1);
-                  v = key >= klo[e >> 1] && key < khi[e >> 1] ? v : -INFINITY;
-                }
-                s[h][e] = v;
-                mx[e >> 1] = fmaxf(mx[e >> 1], v);
+                const int32_t key = key0 + a + r + (e >> 1) * 8;
+                s[e] = key >= klo[e & 1] && key < khi[e & 1] ? s[e] : -INFINITY;
               }
-            bool grow = false;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-              mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-              // the maximum follows only when it grew by more than 2^8: o and l
-              // carry the same factor, so nothing is lost
-              grow |= mx[i] > m[i] + 8.f;
             }
-            if (__any_sync(0xffffffffu, grow)) {
+            float mx[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) {
+              mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], w));
+              mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], w));
+            }
+            // the maximum follows only when it grew by more than 2^8: o and l
+            // carry the same factor, so nothing is lost
+            if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
               float al[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
@@ -372,24 +381,18 @@ __global__ void __launch_bounds__(kThreads, kFewCtasPerSm)
                 l[i] *= al[i];
               }
 #pragma unroll
-              for (int t = 0; t < C::NT; ++t) {
+              for (int t = 0; t < C::MT; ++t) {
                 o[t][0] *= al[0];
-                o[t][1] *= al[0];
-                o[t][2] *= al[1];
+                o[t][1] *= al[1];
+                o[t][2] *= al[0];
                 o[t][3] *= al[1];
               }
             }
+            const float sub[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) sub[i] = m[i] == -INFINITY ? 0.f : m[i];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) s[h][e] = ex2(s[h][e] - sub[e >> 1]);
-              l[0] += s[h][0] + s[h][1];
-              l[1] += s[h][2] + s[h][3];
-              pf[2 * h] = pack_bf16x2(s[h][0], s[h][1]);
-              pf[2 * h + 1] = pack_bf16x2(s[h][2], s[h][3]);
-            }
+            for (int e = 0; e < 4; ++e) s[e] = ex2(s[e] - sub[e & 1]);
+            l[0] += s[0] + s[2];
+            l[1] += s[1] + s[3];
           }
           if (!v_here) {
             v_here = mbar_wait(&sh.full[vs], ((pos + 1) / C::NSLOT) & 1, abort);
@@ -405,48 +408,102 @@ __global__ void __launch_bounds__(kThreads, kFewCtasPerSm)
             keep1 = (in(2 * c + 8) ? 0xffffu : 0u) | (in(2 * c + 9) ? 0xffff0000u : 0u);
           }
           if constexpr (E4M3) {
-            const uint32_t sc0 = lds32(vsc + scale_at(a + 2 * c, box_shift)) & keep0;
-            const uint32_t sc1 = lds32(vsc + scale_at(a + 2 * c + 8, box_shift)) & keep1;
-            const Factor f0 = factor_of(sc0), f1 = factor_of(sc1);
-            const bool rest = __any_sync(0xffffffffu, f0.rest != 0x3f803f80u || f1.rest != 0x3f803f80u);
             uint32_t w[4][D / 32];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t row = a + 2 * c + (k & 1) + (k >> 1) * 8;
               if constexpr (D == 128) {
-                const uint4 u = lds128(vt + swz(row, r * 16));
+                const uint4 u = lds<uint4>(vt + swz(row, r * 16));
                 w[k][0] = u.x;
                 w[k][1] = u.y;
                 w[k][2] = u.z;
                 w[k][3] = u.w;
               } else if constexpr (D == 64) {
-                const uint2 u = lds64(vt + swz(row, r * 8));
+                const uint2 u = lds<uint2>(vt + swz(row, r * 8));
                 w[k][0] = u.x;
                 w[k][1] = u.y;
               } else {
 #pragma unroll
-                for (int i = 0; i < 3; ++i) w[k][i] = lds32(vt + swz(row, r * 12 + i * 4));
+                for (int i = 0; i < 3; ++i) w[k][i] = lds<uint32_t>(vt + swz(row, r * 12 + i * 4));
               }
             }
+            // scales of keys a + r, a + r + 8, the rows of P; 0 stands for a vector that is not there
+            float sv[2];
 #pragma unroll
-            for (int t = 0; t < C::NT; ++t) {
-              constexpr uint32_t kSel[4] = {0x4000u, 0x5010u, 0x6020u, 0x7030u};
-              uint32_t b0 = mul_pair(raw_pair(__byte_perm(w[0][t >> 2], w[1][t >> 2], kSel[t & 3])), f0.f);
-              uint32_t b1 = mul_pair(raw_pair(__byte_perm(w[2][t >> 2], w[3][t >> 2], kSel[t & 3])), f1.f);
-              if (rest) {
-                b0 = mul_pair(b0, f0.rest);
-                b1 = mul_pair(b1, f1.rest);
+            for (int k = 0; k < 2; ++k) sv[k] = __bfloat162float(lds<__nv_bfloat16>(vsc + scale_at(a + r + 8 * k, box_shift)));
+            if (vedge) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                sv[k] = key0 + a + r + 8 * k >= x.u.lo && key0 + a + r + 8 * k < x.u.hi ? sv[k] : 0.f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const bool keep = ((k >> 1) ? keep1 : keep0) & ((k & 1) ? 0xffff0000u : 0xffffu);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) w[k][i] = keep ? w[k][i] : 0u;
               }
-              mma16816(o[t], pf, b0, b1);
+            }
+            auto odd = [&] {
+              const float least = vref * 0x1p-12f;
+              return __any_sync(0xffffffffu, !(sv[0] <= vref) || !(sv[1] <= vref) || (sv[0] < least && sv[0] != 0.f) ||
+                                                 (sv[1] < least && sv[1] != 0.f));
+            };
+            bool wide = odd();
+            if (wide) {  // a new largest scale: o to its units; and look again
+              float top = fmaxf(sv[0], sv[1]);
+#pragma unroll
+              for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+              if (top > vref) {
+                const float f = vref / top;  // powers of two (or 0)
+                vref = top;
+                vinv = 0x1p7f / top;
+#pragma unroll
+                for (int t = 0; t < C::MT; ++t)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[t][e] *= f;
+                wide = odd();
+              }
+            }
+            if (!wide) {
+              const float f0 = sv[0] * vinv, f1 = sv[1] * vinv;
+              const uint32_t p0 = transpose8(pack_f16x2(s[0] * f0, s[1] * f0));
+              const uint32_t p1 = transpose8(pack_f16x2(s[2] * f1, s[3] * f1));
+#pragma unroll
+              for (int t = 0; t < C::MT; ++t) {
+                const uint32_t sel = (t & 1) ? 0x7362u : 0x5140u;
+                const uint32_t u0 = __byte_perm(w[0][t >> 1], w[1][t >> 1], sel);
+                const uint32_t u1 = __byte_perm(w[2][t >> 1], w[3][t >> 1], sel);
+                mma16816<true>(o[t], f16_pair(u0), f16_pair(u0 >> 16), f16_pair(u1), f16_pair(u1 >> 16), p0, p1);
+              }
+            } else {
+              const float up = vref > 0.f ? 1.f / vref : 1.f;
+              // the factors of keys 2c, 2c + 1 and 2c + 8, 2c + 9
+              uint32_t f[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t sc = lds<uint32_t>(vsc + scale_at(a + 2 * c + 8 * k, box_shift)) & (k ? keep1 : keep0);
+                f[k] = pack_bf16x2(bf16_lo(sc) * up * 0x1p127f, bf16_hi(sc) * up * 0x1p127f);
+              }
+              const uint32_t p0 = transpose8(pack_bf16x2(s[0], s[1])), p1 = transpose8(pack_bf16x2(s[2], s[3]));
+#pragma unroll
+              for (int t = 0; t < C::MT; ++t) {
+                uint32_t b[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {  // half-tile k & 1, keys k >> 1
+                  const int y = 2 * t + (k & 1);
+                  constexpr uint32_t kSel[4] = {0x4000u, 0x5010u, 0x6020u, 0x7030u};
+                  b[k] = mul_pair(raw_pair(__byte_perm(w[k & 2][y >> 2], w[(k & 2) + 1][y >> 2], kSel[y & 3])), f[k >> 1]);
+                }
+                mma16816<false>(o[t], b[0], b[1], b[2], b[3], p0, p1);
+              }
             }
           } else {
             const uint32_t row = a + (lane & 15);
+            const uint32_t p0 = transpose8(pack_bf16x2(s[0], s[1])), p1 = transpose8(pack_bf16x2(s[2], s[3]));
 #pragma unroll
-            for (int t = 0; t < C::NT; t += 2) {
+            for (int t = 0; t < C::MT; ++t) {
               uint32_t b[4];
-              ldsm_x4_t(b, vt + (t >> 3) * C::CHUNK + swz(row, ((t & 7) + (lane >> 4)) * 16));
-              mma16816(o[t], pf, b[0] & keep0, b[1] & keep1);
-              mma16816(o[t + 1], pf, b[2] & keep0, b[3] & keep1);
+              ldsm_x4_t(b, smem_addr(vt) + (t >> 2) * C::CHUNK + swz(row, ((2 * t & 7) + (lane >> 4)) * 16));
+              mma16816<false>(o[t], b[0] & keep0, b[2] & keep0, b[1] & keep1, b[3] & keep1, p0, p1);
             }
           }
         }
@@ -455,24 +512,31 @@ __global__ void __launch_bounds__(kThreads, kFewCtasPerSm)
         if (lane == 0) mbar_arrive(&sh.empty[vs]);
       }
       if (!ok) break;
-      // row sums over the four lanes of a row
+      if constexpr (E4M3) {
+        const float f = vref * 0x1p-7f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        for (int t = 0; t < C::MT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][e] *= f;
+      }
+      // row sums over the lanes of a row
+#pragma unroll
+      for (int w = 4; w < 32; w <<= 1) {
+        l[0] += __shfl_xor_sync(0xffffffffu, l[0], w);
+        l[1] += __shfl_xor_sync(0xffffffffu, l[1], w);
       }
       // join the warps that share these rows
       for (int step = share >> 1; step >= 1 && ok; step >>= 1) {
         float* buf = xchg + ((kg & (step - 1)) * mt + rt) * (C::XCHG / 4) + lane;
         if (kg >= step && kg < 2 * step) {
 #pragma unroll
-          for (int t = 0; t < C::NT; ++t)
+          for (int t = 0; t < C::MT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) buf[(t * 4 + e) * 32] = o[t][e];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            buf[(C::NT * 4 + i) * 32] = m[i];
-            buf[(C::NT * 4 + 2 + i) * 32] = l[i];
+            buf[(C::MT * 4 + i) * 32] = m[i];
+            buf[(C::MT * 4 + 2 + i) * 32] = l[i];
           }
         }
         mbar_arrive(&sh.join);
@@ -484,16 +548,16 @@ __global__ void __launch_bounds__(kThreads, kFewCtasPerSm)
           float a0[2], a1[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float m1 = buf[(C::NT * 4 + i) * 32], mn = fmaxf(m[i], m1);
+            const float m1 = buf[(C::MT * 4 + i) * 32], mn = fmaxf(m[i], m1);
             a0[i] = mn == -INFINITY ? 1.f : ex2(m[i] - mn);
             a1[i] = mn == -INFINITY ? 1.f : ex2(m1 - mn);
             m[i] = mn;
-            l[i] = l[i] * a0[i] + buf[(C::NT * 4 + 2 + i) * 32] * a1[i];
+            l[i] = l[i] * a0[i] + buf[(C::MT * 4 + 2 + i) * 32] * a1[i];
           }
 #pragma unroll
-          for (int t = 0; t < C::NT; ++t)
+          for (int t = 0; t < C::MT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[t][e] = o[t][e] * a0[e >> 1] + buf[(t * 4 + e) * 32] * a1[e >> 1];
+            for (int e = 0; e < 4; ++e) o[t][e] = o[t][e] * a0[e & 1] + buf[(t * 4 + e) * 32] * a1[e & 1];
         }
         mbar_arrive(&sh.join);
         if (!mbar_wait(&sh.join, joins++ & 1, abort)) {
@@ -503,56 +567,50 @@ __global__ void __launch_bounds__(kThreads, kFewCtasPerSm)
       }
       if (!ok) break;
       if (kg != 0 || !works) continue;
-      // column of element e of n-tile t: d_of(t, e & 1)
-      auto d_of = [&](int t, int e) { return E4M3 ? (2 * c + e) * (D / 8) + t : t * 8 + 2 * c + e; };
-      if (x.whole()) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!live[i]) continue;
+      for (int i = 0; i < 2; ++i) {
+        const int32_t rr = rt * 8 + 2 * c + i;  // row of the unit; this lane's columns of it:
+        if (rr >= rows) continue;
+        if (x.whole()) {
+          const int32_t at = skip + rr, t0 = at / p.group, hd = x.kh * p.group + at - t0 * p.group;
+          const int64_t row = x.q0 + x.u.t0 + t0;
           const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);  // no key: 0; NaN stays
-          __nv_bfloat16* oa = p.out + (int64_t)(x.q0 + tok[i]) * p.o_rs + (int64_t)hd[i] * p.o_hs;
-          if constexpr (E4M3) {
+          __nv_bfloat16* oa = p.out + row * p.o_rs + (int64_t)hd * p.o_hs;
+          if constexpr (E4M3) {  // D/8 consecutive ones
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int t = 0; t < C::NT; t += 4) {
-                const uint2 w = make_uint2(pack_bf16x2(o[t][2 * i + e] * inv, o[t + 1][2 * i + e] * inv),
-                                           pack_bf16x2(o[t + 2][2 * i + e] * inv, o[t + 3][2 * i + e] * inv));
-                __nv_bfloat16* a = oa + d_of(t, e);
-                if (in_span(p.out_span, a, 8, p.err)) *reinterpret_cast<uint2*>(a) = w;
-              }
-          } else {
-#pragma unroll
-            for (int t = 0; t < C::NT; ++t) {
-              __nv_bfloat16* a = oa + d_of(t, 0);
-              if (in_span(p.out_span, a, 4, p.err))
-                *reinterpret_cast<uint32_t*>(a) = pack_bf16x2(o[t][2 * i] * inv, o[t][2 * i + 1] * inv);
+            for (int t = 0; t < C::MT; t += 2) {
+              __nv_bfloat16* d = oa + r * (D / 8) + 2 * t;
+              if (in_span(p.out_span, d, 8, p.err))
+                *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16x2(o[t][i] * inv, o[t][2 + i] * inv),
+                                                          pack_bf16x2(o[t + 1][i] * inv, o[t + 1][2 + i] * inv));
             }
-          }
-          float* la = p.lse + (int64_t)hd[i] * p.total_q + x.q0 + tok[i];
-          if (c == 0 && in_span(p.lse_span, la, 4, p.err))
-            *la = l[i] == 0.f ? -INFINITY : (m[i] + __log2f(l[i])) * 0.69314718055994531f;
-        }
-      } else {
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (x.begins() ? 1 : 0);
+          } else {  // r, r + 8 of each 16
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!live[i]) continue;
-          const int64_t row = slot * parts.rows + rt * 16 + r + i * 8;
+            for (int t = 0; t < C::MT; ++t)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                __nv_bfloat16* d = oa + t * 16 + e * 8 + r;
+                if (in_span(p.out_span, d, 2, p.err)) *d = __float2bfloat16_rn(o[t][2 * e + i] * inv);
+              }
+          }
+          float* la = p.lse + (int64_t)hd * p.total_q + row;
+          if (r == 0 && in_span(p.lse_span, la, 4, p.err))
+            *la = l[i] == 0.f ? -INFINITY : (m[i] + __log2f(l[i])) * 0.69314718055994531f;
+        } else {
+          const int64_t row = (2 * (int64_t)blockIdx.x + (x.begins() ? 1 : 0)) * parts.rows + rr;
           float* oa = parts.o + row * D;
           if constexpr (E4M3) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int t = 0; t < C::NT; t += 4)
-                *reinterpret_cast<float4*>(oa + d_of(t, e)) =
-                    make_float4(o[t][2 * i + e], o[t + 1][2 * i + e], o[t + 2][2 * i + e], o[t + 3][2 * i + e]);
+            for (int t = 0; t < C::MT; t += 2)
+              *reinterpret_cast<float4*>(oa + r * (D / 8) + 2 * t) =
+                  make_float4(o[t][i], o[t][2 + i], o[t + 1][i], o[t + 1][2 + i]);
           } else {
 #pragma unroll
-            for (int t = 0; t < C::NT; ++t)
-              *reinterpret_cast<float2*>(oa + d_of(t, 0)) = make_float2(o[t][2 * i], o[t][2 * i + 1]);
+            for (int t = 0; t < C::MT; ++t)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) oa[t * 16 + e * 8 + r] = o[t][2 * e + i];
           }
-          if (c == 0) *reinterpret_cast<float2*>(parts.ml + row * 2) = make_float2(m[i], l[i]);
+          if (r == 0) *reinterpret_cast<float2*>(parts.ml + row * 2) = make_float2(m[i], l[i]);
         }
       }
     }
@@ -567,7 +625,7 @@ cudaError_t launch_few_d(const PagedLaunch& L, int32_t take, cudaStream_t stream
   auto kern = varlen_paged_few_kernel<D, E4M3>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(kern, (unsigned)(L.sms * kFewCtasPerSm), kThreads, C::SMEM, stream, L.few_k, L.few_v, L.few_ks,
+  return launch_overlapped(kern, (unsigned)(L.sms * kFewCtasPerSm), C::THREADS, C::SMEM, stream, L.few_k, L.few_v, L.few_ks,
                            L.few_vs, L.p, L.few, take);
 }
 

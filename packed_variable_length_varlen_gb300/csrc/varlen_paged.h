@@ -107,9 +107,9 @@ struct PagedParams {
 enum PagedTake : int32_t { kTakeFew = 0, kTakeMany = 1, kTakeAll = 2 };
 
 constexpr int kFewRows = 32;      // rows (queries x heads of a group) of a unit of the kernel for few rows
-// keys per tile of that kernel: 16 KB of K at D = 128, in either type
-constexpr int few_tile(bool e4m3) { return e4m3 ? 128 : 64; }
-constexpr int kFewCtasPerSm = 2;
+constexpr int kFewTile = 64;      // keys per tile of that kernel
+// its CTAs on an SM: E4M3 rows are half as long, so more of them have to be in the making
+constexpr int few_ctas(bool e4m3) { return e4m3 ? 3 : 2; }
 constexpr int kMaxSms = 160;      // the workspace is sized for this many
 
 // What CTA c left for the join: the unit that it begins and does not end, and
@@ -125,14 +125,15 @@ struct PagedParts {
   float* o;
   float* ml;
   PagedJoin* join;
-  int32_t rows;
+  int32_t rows;       // rows of a slot
+  int32_t unit_rows;  // rows of a unit
 };
 
 struct PagedLaunch {
   PagedParams p;
   int head_dim, sms;
   bool e4m3, few_only;
-  CUtensorMap few_k, few_v, few_ks, few_vs;  // pages and (E4M3) scales in boxes of up to few_tile keys
+  CUtensorMap few_k, few_v, few_ks, few_vs;  // pages and (E4M3) scales in boxes of up to kFewTile keys
   PagedParts few;
 };
 
@@ -145,7 +146,7 @@ inline PagedWorkspace paged_workspace(int64_t total_rows, int32_t head_dim) {
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   PagedWorkspace w;
   w.few_rows = (int32_t)(total_rows < kFewRows ? (total_rows < 1 ? 1 : total_rows) : kFewRows);
-  const size_t ctas = (size_t)kFewCtasPerSm * kMaxSms;
+  const size_t ctas = (size_t)few_ctas(true) * kMaxSms;
   w.few_o = 0;
   w.few_ml = up(w.few_o + 2 * ctas * w.few_rows * head_dim * 4);
   w.few_join = up(w.few_ml + 2 * ctas * w.few_rows * 8);

@@ -240,8 +240,8 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   char* ws = static_cast<char*>(workspace);
   const PagedWorkspace w = paged_workspace((int64_t)total_q * p.group, c.head_dim);
   L.few = PagedParts{reinterpret_cast<float*>(ws + w.few_o), reinterpret_cast<float*>(ws + w.few_ml),
-                     reinterpret_cast<PagedJoin*>(ws + w.few_join), w.few_rows};
-  const int box = std::min(c.page_size, few_tile(L.e4m3));
+                     reinterpret_cast<PagedJoin*>(ws + w.few_join), w.few_rows, kFewRows};
+  const int box = std::min(c.page_size, kFewTile);
   if ((st = encode_pages(&L.few_k, c, c.k, c.sk, box)) != VARLEN_OK) return st;
   if ((st = encode_pages(&L.few_v, c, c.v, c.sv, box)) != VARLEN_OK) return st;
   if (L.e4m3) {

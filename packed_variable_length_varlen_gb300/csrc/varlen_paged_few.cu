@@ -54,16 +54,16 @@ constexpr int kMaxSlots = 8;
 
 template <int D, bool E4M3>
 struct FewCfg {
-  static constexpr int WARPS = E4M3 ? 8 : 4;                // consumer warps
+  static constexpr int WARPS = 4;                           // consumer warps
   static constexpr int THREADS = (WARPS + 1) * 32;
-  static constexpr int KT = few_tile(E4M3);                 // keys per tile
+  static constexpr int KT = kFewTile;                       // keys per tile
   static constexpr int STEP = 16;                           // keys a warp takes at a time
   using Geom = PagedGeom<kFewRows, KT, false>;
   static constexpr int CK = E4M3 ? 1 : (D + 63) / 64;       // 128-byte column chunks of a row
   static constexpr int CHUNK = KT * 128;
   static constexpr int TILE = CK * CHUNK;
   static constexpr int SCALES = E4M3 ? KT * 8 : 0;          // page pieces of at least 16 keys, 128 bytes apart
-  static constexpr int NSLOT = !E4M3 && CK == 1 ? 8 : 5;
+  static constexpr int NSLOT = E4M3 ? 7 : (CK == 1 ? 8 : 5);
   static constexpr int KSTEPS = E4M3 ? (D == 64 ? 4 : 8) : CK * 4;
   static constexpr int MT = D / 16;                         // m-tiles of O^T
   static constexpr int XCHG = (MT * 4 + 4) * 32 * 4;        // one warp's (o, m, l)
@@ -106,6 +106,12 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
+// mbar_wait by a whole warp, its outcome the same in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
 template <class T>
 __device__ __forceinline__ T lds(const uint8_t* p) {
   return *reinterpret_cast<const T*>(p);
@@ -124,11 +130,11 @@ __device__ __forceinline__ uint32_t mul_pair(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
-// Two codes (the low 16 bits of w) as f16.
-__device__ __forceinline__ uint32_t f16_pair(uint32_t w) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(w));
-  return h;
+// Four codes as f16: the first two and the last two.
+__device__ __forceinline__ void f16_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t h;
@@ -145,7 +151,7 @@ __device__ __forceinline__ uint32_t scale_at(uint32_t r, int shift) {
 }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, kFewCtasPerSm)
+__global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
     varlen_paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                             const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
                             const PagedParams p, const PagedParts parts, int32_t take) {
@@ -160,7 +166,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, kFewCtasPerSm)
   uint8_t* scales = ring + C::NSLOT * C::TILE;
   float* xchg = reinterpret_cast<float*>(scales + C::NSLOT * C::SCALES);
   volatile int* abort = &sh.abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_id(), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NSLOT; ++i) {
       mbar_init(&sh.full[i], 1);
@@ -175,7 +181,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, kFewCtasPerSm)
   dependents_may_launch();
   PagedWalk<typename C::Geom> walk;
   PagedPiece x;
-  const int box_shift = min(p.pages.page_shift, E4M3 ? 7 : 6);  // keys of one page piece of a tile
+  const int box_shift = min(p.pages.page_shift, 6);  // keys of one page piece of a tile
 
   if (warp == C::WARPS) {
     // ------------------------------------------------------------ producer
@@ -299,7 +305,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, kFewCtasPerSm)
       const int32_t tiles = min(x.j1, x.u.tiles);
       for (int32_t j = x.j0; j < tiles; ++j, pos += 2) {
         const uint32_t ks = pos % C::NSLOT, vs = (pos + 1) % C::NSLOT;
-        if (!mbar_wait(&sh.full[ks], (pos / C::NSLOT) & 1, abort)) {
+        if (!warp_wait(&sh.full[ks], (pos / C::NSLOT) & 1, abort)) {
           ok = false;
           break;
         }
@@ -332,9 +338,12 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, kFewCtasPerSm)
               if constexpr (E4M3) {
                 const uint32_t x0[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, x1[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma16816<true>((k & 1) ? s2 : s, f16_pair(x0[k]), f16_pair(x1[k]), f16_pair(x0[k] >> 16),
-                                 f16_pair(x1[k] >> 16), qf[i * 4 + k][0], qf[i * 4 + k][1]);
+                for (int k = 0; k < 4; ++k) {
+                  uint32_t a0, a1, a2, a3;
+                  f16_pairs(x0[k], a0, a2);
+                  f16_pairs(x1[k], a1, a3);
+                  mma16816<true>((k & 1) ? s2 : s, a0, a1, a2, a3, qf[i * 4 + k][0], qf[i * 4 + k][1]);
+                }
               } else {
                 mma16816<false>(s, u[i].x, v[i].x, u[i].y, v[i].y, qf[2 * i][0], qf[2 * i][1]);
                 mma16816<false>(s2, u[i].z, v[i].z, u[i].w, v[i].w, qf[2 * i + 1][0], qf[2 * i + 1][1]);
@@ -395,7 +404,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, kFewCtasPerSm)
             l[1] += s[1] + s[3];
           }
           if (!v_here) {
-            v_here = mbar_wait(&sh.full[vs], ((pos + 1) / C::NSLOT) & 1, abort);
+            v_here = warp_wait(&sh.full[vs], ((pos + 1) / C::NSLOT) & 1, abort);
             ok = ok && v_here;
           }
           if (!ok) break;
@@ -472,7 +481,10 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, kFewCtasPerSm)
                 const uint32_t sel = (t & 1) ? 0x7362u : 0x5140u;
                 const uint32_t u0 = __byte_perm(w[0][t >> 1], w[1][t >> 1], sel);
                 const uint32_t u1 = __byte_perm(w[2][t >> 1], w[3][t >> 1], sel);
-                mma16816<true>(o[t], f16_pair(u0), f16_pair(u0 >> 16), f16_pair(u1), f16_pair(u1 >> 16), p0, p1);
+                uint32_t a0, a1, a2, a3;
+                f16_pairs(u0, a0, a1);
+                f16_pairs(u1, a2, a3);
+                mma16816<true>(o[t], a0, a1, a2, a3, p0, p1);
               }
             } else {
               const float up = vref > 0.f ? 1.f / vref : 1.f;
@@ -540,7 +552,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, kFewCtasPerSm)
           }
         }
         mbar_arrive(&sh.join);
-        if (!mbar_wait(&sh.join, joins++ & 1, abort)) {
+        if (!warp_wait(&sh.join, joins++ & 1, abort)) {
           ok = false;
           break;
         }
@@ -560,7 +572,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, kFewCtasPerSm)
             for (int e = 0; e < 4; ++e) o[t][e] = o[t][e] * a0[e & 1] + buf[(t * 4 + e) * 32] * a1[e & 1];
         }
         mbar_arrive(&sh.join);
-        if (!mbar_wait(&sh.join, joins++ & 1, abort)) {
+        if (!warp_wait(&sh.join, joins++ & 1, abort)) {
           ok = false;
           break;
         }
@@ -625,7 +637,7 @@ cudaError_t launch_few_d(const PagedLaunch& L, int32_t take, cudaStream_t stream
   auto kern = varlen_paged_few_kernel<D, E4M3>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(kern, (unsigned)(L.sms * kFewCtasPerSm), C::THREADS, C::SMEM, stream, L.few_k, L.few_v, L.few_ks,
+  return launch_overlapped(kern, (unsigned)(L.sms * few_ctas(E4M3)), C::THREADS, C::SMEM, stream, L.few_k, L.few_v, L.few_ks,
                            L.few_vs, L.p, L.few, take);
 }
 

@@ -90,10 +90,71 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   }
 }
 
+// The same for the kernel for many rows, whose units have 256 rows and mostly
+// few parts: a warp takes a row.
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    varlen_paged_join_rows_kernel(const PagedParams p, const PagedParts parts) {
+  __shared__ float weights[kJoinWarps][kMaxSms];
+  dependency_wait();
+  const PagedJoin u = parts.join[blockIdx.x];
+  dependents_may_launch();
+  if (u.parts == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* weight = weights[warp];
+  const int32_t q0 = clamp_row(__ldg(p.cu_q + u.b), p.total_q), q1 = clamp_row(__ldg(p.cu_q + u.b + 1), p.total_q);
+  const int32_t half_tokens = kChunkRows / 2 / p.group;
+  for (int32_t row = blockIdx.y * kJoinWarps + warp; row < kChunkRows; row += gridDim.y * kJoinWarps) {
+    const int32_t half = row >> 7, in_half = row & 127, t = in_half / p.group;
+    const int64_t tok = (int64_t)u.blk * 2 * half_tokens + half * half_tokens + t;
+    if (t >= half_tokens || tok >= q1 - q0) continue;
+    auto at = [&](int32_t k) { return (2 * ((int64_t)blockIdx.x + k) + (k == 0 ? 1 : 0)) * parts.rows + row; };
+    float m = -INFINITY, l = 0.f;
+    for (int32_t k = lane; k < u.parts; k += 32) {
+      weight[k] = parts.ml[at(k) * 2];
+      m = fmaxf(m, weight[k]);
+    }
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+    const float ref = m == -INFINITY ? 0.f : m;
+    for (int32_t k = lane; k < u.parts; k += 32) {
+      weight[k] = ex2(weight[k] - ref);
+      l += parts.ml[at(k) * 2 + 1] * weight[k];
+    }
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+    __syncwarp();
+    float o[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+#pragma unroll 4
+    for (int32_t k = 0; k < u.parts; ++k) {
+      const float* oa = parts.o + at(k) * D + lane;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(oa[i * 32], weight[k], o[i]);
+    }
+    __syncwarp();
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    const int32_t hd = u.kh * p.group + in_half - t * p.group;
+    __nv_bfloat16* a = p.out + (q0 + tok) * p.o_rs + (int64_t)hd * p.o_hs + lane;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+      if (in_span(p.out_span, a + i * 32, 2, p.err)) a[i * 32] = __float2bfloat16_rn(o[i] * inv);
+    float* la = p.lse + (int64_t)hd * p.total_q + q0 + tok;
+    if (lane == 0 && in_span(p.lse_span, la, 4, p.err))
+      *la = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+  }
+}
+
 template <int D>
 cudaError_t launch_join_d(const PagedLaunch& L, cudaStream_t stream) {
-  return launch_overlapped(varlen_paged_join_kernel<D>, dim3(L.sms * few_ctas(L.e4m3), kJoinRows), kJoinWarps * 32,
-                           0, stream, L.p, L.few);
+  cudaError_t e = cudaSuccess;
+  if (L.few)
+    e = launch_overlapped(varlen_paged_join_kernel<D>, dim3(L.sms * few_ctas(L.e4m3), kJoinRows), kJoinWarps * 32, 0,
+                          stream, L.p, L.few_parts);
+  if (e == cudaSuccess && L.many)
+    e = launch_overlapped(varlen_paged_join_rows_kernel<D>, dim3(L.sms, 8), kJoinWarps * 32, 0, stream, L.p, L.chunk);
+  return e;
 }
 
 }  // namespace
@@ -108,9 +169,10 @@ cudaError_t launch_paged_join(const PagedLaunch& L, cudaStream_t stream) {
 }
 
 cudaError_t launch_paged(const PagedLaunch& L, cudaStream_t stream) {
-  const cudaError_t e = launch_paged_few(L, kTakeAll, stream);
-  if (e != cudaSuccess) return e;
-  return launch_paged_join(L, stream);
+  cudaError_t e = cudaSuccess;
+  if (L.many) e = launch_paged_chunk(L, L.few ? kTakeMany : kTakeAll, stream);
+  if (e == cudaSuccess && L.few) e = launch_paged_few(L, L.many ? kTakeFew : kTakeAll, stream);
+  return e == cudaSuccess ? launch_paged_join(L, stream) : e;
 }
 
 }  // namespace varlen

@@ -110,6 +110,8 @@ constexpr int kFewRows = 32;      // rows (queries x heads of a group) of a unit
 constexpr int kFewTile = 64;      // keys per tile of that kernel
 // its CTAs on an SM: E4M3 rows are half as long, so more of them have to be in the making
 constexpr int few_ctas(bool e4m3) { return e4m3 ? 3 : 2; }
+constexpr int kChunkRows = 256;   // rows of a unit of the kernel for many rows (two halves)
+constexpr int kChunkTile = 128;   // keys per tile of that kernel
 constexpr int kMaxSms = 160;      // the workspace is sized for this many
 
 // What CTA c left for the join: the unit that it begins and does not end, and
@@ -132,25 +134,37 @@ struct PagedParts {
 struct PagedLaunch {
   PagedParams p;
   int head_dim, sms;
-  bool e4m3, few_only;
+  bool e4m3;
+  bool few, many;  // which kernels run; alone, each takes every segment
   CUtensorMap few_k, few_v, few_ks, few_vs;  // pages and (E4M3) scales in boxes of up to kFewTile keys
-  PagedParts few;
+  CUtensorMap chunk_q;                       // {D, group, key heads, rows}, boxes of half a unit
+  CUtensorMap chunk_k, chunk_v, chunk_ks, chunk_vs;  // the cache in boxes of up to kChunkTile keys
+  PagedParts few_parts, chunk;
 };
 
-// Byte offsets of the workspace.
+// Byte offsets of the workspace.  (A call whose rows all together are no more
+// than kFewRows has no segment for the kernel for many rows.)
 struct PagedWorkspace {
-  size_t few_o, few_ml, few_join, bytes;
+  size_t few_o, few_ml, few_join, chunk_o, chunk_ml, chunk_join, bytes;
   int32_t few_rows;
 };
 inline PagedWorkspace paged_workspace(int64_t total_rows, int32_t head_dim) {
-  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  size_t at = 0;
+  auto take = [&at](size_t bytes) {
+    const size_t a = at;
+    at += (bytes + 255) & ~size_t(255);
+    return a;
+  };
   PagedWorkspace w;
   w.few_rows = (int32_t)(total_rows < kFewRows ? (total_rows < 1 ? 1 : total_rows) : kFewRows);
-  const size_t ctas = (size_t)few_ctas(true) * kMaxSms;
-  w.few_o = 0;
-  w.few_ml = up(w.few_o + 2 * ctas * w.few_rows * head_dim * 4);
-  w.few_join = up(w.few_ml + 2 * ctas * w.few_rows * 8);
-  w.bytes = up(w.few_join + ctas * sizeof(PagedJoin));
+  const size_t few = (size_t)few_ctas(true) * kMaxSms, many = total_rows > kFewRows ? kMaxSms : 0;
+  w.few_o = take(2 * few * w.few_rows * head_dim * 4);
+  w.few_ml = take(2 * few * w.few_rows * 8);
+  w.few_join = take(few * sizeof(PagedJoin));
+  w.chunk_o = take(2 * many * kChunkRows * head_dim * 4);
+  w.chunk_ml = take(2 * many * kChunkRows * 8);
+  w.chunk_join = take(many * sizeof(PagedJoin));
+  w.bytes = at;
   return w;
 }
 
@@ -173,6 +187,7 @@ cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, unsigned threads, s
 }
 
 cudaError_t launch_paged_few(const PagedLaunch& L, int32_t take, cudaStream_t stream);
+cudaError_t launch_paged_chunk(const PagedLaunch& L, int32_t take, cudaStream_t stream);
 cudaError_t launch_paged_join(const PagedLaunch& L, cudaStream_t stream);
 cudaError_t launch_paged(const PagedLaunch& L, cudaStream_t stream);
 

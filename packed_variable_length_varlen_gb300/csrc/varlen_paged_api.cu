@@ -92,6 +92,18 @@ int encode_scales(CUtensorMap* map, const varlen_kv_cache& c, const void* base, 
   return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, false);
 }
 
+// Queries as {D, heads of a group, key heads, rows} in boxes of 64 columns of
+// all rows of 128 / group tokens of one key head.
+int encode_queries(CUtensorMap* map, const void* base, varlen_stride s, int32_t rows, int32_t kv_heads, int32_t group,
+                   int32_t D) {
+  // (a stride over one element is never used: a legal value for it)
+  const cuuint64_t head = (int64_t)kv_heads * group > 1 ? s.head * 2 : D * 2, row = rows > 1 ? s.row * 2 : D * 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)group, (cuuint64_t)kv_heads, (cuuint64_t)rows};
+  const cuuint64_t strides[3] = {head, head * group, row};
+  const cuuint32_t box[4] = {64u, (cuuint32_t)group, 1u, (cuuint32_t)(kChunkRows / 2 / group)};
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, true);
+}
+
 int cache_impl(const void* k, varlen_stride sk, const void* v, varlen_stride sv, const int32_t* cu, int32_t batch,
                int32_t total, const varlen_kv_cache* cache, void* stream, bool write) {
   int shift = 0;
@@ -235,18 +247,31 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   L.head_dim = c.head_dim;
   L.sms = std::min(sms, kMaxSms);
   L.e4m3 = c.type == VARLEN_CACHE_E4M3;
-  L.few_only = (int64_t)total_q * p.group <= kFewRows ||
-               (max_seqlen_q > 0 && (int64_t)max_seqlen_q * p.group <= kFewRows);
+  // Which kernels: where every segment is known to have few rows, that one
+  // alone; a single segment of more rows goes to the other one whatever its
+  // length; otherwise both run and each takes the segments that are its own.
+  const int64_t total_rows = (int64_t)total_q * p.group;
+  L.few = total_rows <= kFewRows || batch > 1 || (max_seqlen_q > 0 && (int64_t)max_seqlen_q * p.group <= kFewRows);
+  L.many = total_rows > kFewRows && !(max_seqlen_q > 0 && (int64_t)max_seqlen_q * p.group <= kFewRows);
   char* ws = static_cast<char*>(workspace);
-  const PagedWorkspace w = paged_workspace((int64_t)total_q * p.group, c.head_dim);
-  L.few = PagedParts{reinterpret_cast<float*>(ws + w.few_o), reinterpret_cast<float*>(ws + w.few_ml),
-                     reinterpret_cast<PagedJoin*>(ws + w.few_join), w.few_rows, kFewRows};
-  const int box = std::min(c.page_size, kFewTile);
-  if ((st = encode_pages(&L.few_k, c, c.k, c.sk, box)) != VARLEN_OK) return st;
-  if ((st = encode_pages(&L.few_v, c, c.v, c.sv, box)) != VARLEN_OK) return st;
-  if (L.e4m3) {
-    if ((st = encode_scales(&L.few_ks, c, c.k_scale, box)) != VARLEN_OK) return st;
-    if ((st = encode_scales(&L.few_vs, c, c.v_scale, box)) != VARLEN_OK) return st;
+  const PagedWorkspace w = paged_workspace(total_rows, c.head_dim);
+  L.few_parts = PagedParts{reinterpret_cast<float*>(ws + w.few_o), reinterpret_cast<float*>(ws + w.few_ml),
+                           reinterpret_cast<PagedJoin*>(ws + w.few_join), w.few_rows, kFewRows};
+  L.chunk = PagedParts{reinterpret_cast<float*>(ws + w.chunk_o), reinterpret_cast<float*>(ws + w.chunk_ml),
+                       reinterpret_cast<PagedJoin*>(ws + w.chunk_join), kChunkRows, kChunkRows};
+  auto maps = [&](CUtensorMap* k, CUtensorMap* v, CUtensorMap* ks, CUtensorMap* vs, int tile) {
+    const int box = std::min(c.page_size, tile);
+    int s2;
+    if ((s2 = encode_pages(k, c, c.k, c.sk, box)) != VARLEN_OK || (s2 = encode_pages(v, c, c.v, c.sv, box)) != VARLEN_OK)
+      return s2;
+    if (!L.e4m3) return (int)VARLEN_OK;
+    if ((s2 = encode_scales(ks, c, c.k_scale, box)) != VARLEN_OK) return s2;
+    return encode_scales(vs, c, c.v_scale, box);
+  };
+  if (L.few && (st = maps(&L.few_k, &L.few_v, &L.few_ks, &L.few_vs, kFewTile)) != VARLEN_OK) return st;
+  if (L.many) {
+    if ((st = maps(&L.chunk_k, &L.chunk_v, &L.chunk_ks, &L.chunk_vs, kChunkTile)) != VARLEN_OK) return st;
+    if ((st = encode_queries(&L.chunk_q, q, sq, total_q, c.num_kv_heads, p.group, c.head_dim)) != VARLEN_OK) return st;
   }
   const cudaError_t e = launch_paged(L, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VARLEN_OK : cuda_fail(e);

@@ -638,7 +638,7 @@ cudaError_t launch_few_d(const PagedLaunch& L, int32_t take, cudaStream_t stream
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_overlapped(kern, (unsigned)(L.sms * few_ctas(E4M3)), C::THREADS, C::SMEM, stream, L.few_k, L.few_v, L.few_ks,
-                           L.few_vs, L.p, L.few, take);
+                           L.few_vs, L.p, L.few_parts, take);
 }
 
 }  // namespace

@@ -13,6 +13,7 @@ that allocate outputs / workspace with torch on the inputs' device and raise
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -642,46 +643,64 @@ class PagedCache:
         c.type = VARLEN_CACHE_E4M3 if e4m3 else VARLEN_CACHE_BF16
         c.num_pages, c.page_size, c.num_kv_heads, c.head_dim = pages, page_size, heads, dim
         c.max_pages = block_table.shape[1]
-        self.struct = c
+        self.struct, self.ref = c, ctypes.byref(c)
 
 
-def _check_packed(cache, cu_seqlens, *tensors):
-    """Types and places that the C entry points cannot see."""
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() \
-            or cu_seqlens.shape[0] != cache.batch + 1:
+def _packed(cache, t, heads, rows=None):
+    """(pointer, strides) of packed rows t, checked for what the C entry
+    points cannot see: type, shape, place."""
+    n, h, d = t.shape
+    st = t.stride()
+    if t.dtype != torch.bfloat16 or h != heads or d != cache.head_dim or st[2] != 1 or (rows is not None and n != rows):
+        raise ValueError("packed rows must be bfloat16 [rows, heads, head_dim] with unit innermost stride (here %s "
+                         "heads of %d%s)" % (heads, cache.head_dim, "" if rows is None else ", %d rows" % rows))
+    if t.device != cache.device:
+        raise ValueError("every tensor must be on the cache's device")
+    return t.data_ptr(), VarlenStride(st[0], st[1])
+
+
+def _cu(cache, cu):
+    if cu.dtype != torch.int32 or cu.dim() != 1 or cu.shape[0] != cache.batch + 1 or not cu.is_contiguous():
         raise ValueError("cu_seqlens must be contiguous int32 [batch + 1]")
-    for t in (cu_seqlens,) + tensors:
-        if t.device != cache.device:
-            raise ValueError("every tensor must be on the cache's device")
-    for t in tensors:
-        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != cache.head_dim or t.stride(2) != 1:
-            raise ValueError("packed rows must be bfloat16 [rows, heads, head_dim] with unit innermost stride")
+    if cu.device != cache.device:
+        raise ValueError("every tensor must be on the cache's device")
+    return cu.data_ptr()
 
 
-def _launch(cache, stream, call, where, *fresh):
-    """Runs call(stream) with the cache's device current; tensors allocated
-    for the call (`fresh`) are kept from reuse until `stream` is done."""
-    if cache.device.type != "cuda":
+def _paged_call(entry, cache, stream, fresh, args):
+    """Runs a C entry point with the cache's device current.  Tensors that the
+    call allocated (`fresh`) belong to the current stream: another `stream`
+    waits for it (their memory may still be in use there), and they are kept
+    from reuse until `stream` is done with them."""
+    dev = cache.device.index
+    if dev is None:
         raise ValueError("the cache must be on a CUDA device")
-    if cache.device.index is not None and cache.device.index != torch.cuda.current_device():
-        with torch.cuda.device(cache.device):
-            return _launch(cache, stream, call, where, *fresh)
+    handle = here = torch._C._cuda_getCurrentRawStream(dev)
     if stream is not None:
-        own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if handle != here and fresh:
+        own = torch.cuda.ExternalStream(handle, device=cache.device)
+        own.wait_stream(torch.cuda.current_stream(cache.device))
         for t in fresh:
             t.record_stream(own)
-    _check(call(stream), where)
+    if dev == torch.cuda.current_device():
+        st = entry(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = entry(*args, handle)
+    if st != VARLEN_OK:
+        raise VarlenError(st, entry.__name__)
 
 
 def cache_write(cache, k, v, cu_seqlens, stream=None):
     """Writes packed new rows k, v ([rows, num_kv_heads, D] bf16) into the
     cache: the rows of segment b become the last ones of its seqlens[b]
     positions (seqlens already counts them)."""
-    _check_packed(cache, cu_seqlens, k, v)
-    if k.shape != v.shape or k.shape[1] != cache.num_kv_heads:
-        raise ValueError("k and v must be [rows, num_kv_heads, head_dim]")
-    _launch(cache, stream, lambda s: varlen_attn_cache_write(k, v, cu_seqlens, cache.batch, k.shape[0], cache.struct,
-                                                             s), "varlen_attn_cache_write")
+    kp, ks = _packed(cache, k, cache.num_kv_heads)
+    rows = k.shape[0]
+    vp, vs = _packed(cache, v, cache.num_kv_heads, rows)
+    _paged_call(LIB.varlen_attn_cache_write, cache, stream, (),
+                (kp, ks, vp, vs, _cu(cache, cu_seqlens), cache.batch, rows, cache.ref))
 
 
 def cache_read(cache, cu_seqlens, total, k=None, v=None, stream=None):
@@ -689,17 +708,21 @@ def cache_read(cache, cu_seqlens, total, k=None, v=None, stream=None):
     ([total, num_kv_heads, D], allocated when None); returns (k, v)."""
     fresh = []
     if k is None:
-        k = torch.empty(total, cache.num_kv_heads, cache.head_dim, dtype=torch.bfloat16, device=cache.device)
+        k = torch.empty((total, cache.num_kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device)
         fresh.append(k)
     if v is None:
-        v = torch.empty(total, cache.num_kv_heads, cache.head_dim, dtype=torch.bfloat16, device=cache.device)
+        v = torch.empty((total, cache.num_kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device)
         fresh.append(v)
-    _check_packed(cache, cu_seqlens, k, v)
-    if tuple(k.shape[:2]) != (total, cache.num_kv_heads) or k.shape != v.shape:
-        raise ValueError("k and v must be [total, num_kv_heads, head_dim]")
-    _launch(cache, stream, lambda s: varlen_attn_cache_read(cache.struct, cu_seqlens, cache.batch, total, k, v, s),
-            "varlen_attn_cache_read", *fresh)
+    kp, ks = _packed(cache, k, cache.num_kv_heads, total)
+    vp, vs = _packed(cache, v, cache.num_kv_heads, total)
+    _paged_call(LIB.varlen_attn_cache_read, cache, stream, fresh,
+                (cache.ref, _cu(cache, cu_seqlens), cache.batch, total, kp, ks, vp, vs))
     return k, v
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_workspace_bytes(batch, total_q, num_heads, num_kv_heads, head_dim):
+    return varlen_attn_fwd_paged_workspace_size(batch, total_q, num_heads, num_kv_heads, head_dim)
 
 
 def attention_fwd_paged(q, cache, cu_seqlens_q, max_seqlen_q=0, scale=None, out=None, lse=None, workspace=None,
@@ -708,27 +731,30 @@ def attention_fwd_paged(q, cache, cu_seqlens_q, max_seqlen_q=0, scale=None, out=
     cache's heads) over the cache, the last query of a segment at its
     sequence's last position; `causal` / `window` as in attention_fwd.
     max_seqlen_q, where known, lets short calls run on fewer kernels."""
-    _check_packed(cache, cu_seqlens_q, q)
     total_q, H, D = q.shape
-    scale = float(D ** -0.5) if scale is None else float(scale)
+    qp, qs = _packed(cache, q, H)
+    cu = _cu(cache, cu_seqlens_q)
     fresh = []
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = torch.empty((total_q, H, D), dtype=torch.bfloat16, device=q.device)
         fresh.append(out)
+    op, os_ = _packed(cache, out, H, total_q)
     if lse is None:
-        lse = torch.empty(H, total_q, dtype=torch.float32, device=q.device)
+        lse = torch.empty((H, total_q), dtype=torch.float32, device=q.device)
         fresh.append(lse)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (H, total_q) or not lse.is_contiguous() \
+            or lse.device != cache.device:
+        raise ValueError("lse must be contiguous float32 [H, rows] on the cache's device")
     if workspace is None:
-        nbytes = varlen_attn_fwd_paged_workspace_size(cache.batch, total_q, H, cache.num_kv_heads, D)
+        nbytes = _paged_workspace_bytes(cache.batch, total_q, H, cache.num_kv_heads, D)
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
         fresh.append(workspace)
-    _check_packed(cache, cu_seqlens_q, out)
-    if out.shape != q.shape or lse.dtype != torch.float32 or tuple(lse.shape) != (H, total_q) \
-            or not lse.is_contiguous() or lse.device != q.device or workspace.device != q.device:
-        raise ValueError("out must have q's shape, lse be contiguous float32 [H, rows], all on q's device")
+    else:
+        if workspace.device != cache.device:
+            raise ValueError("the workspace must be on the cache's device")
+        nbytes = workspace.numel() * workspace.element_size()
     left, right = _band(causal, window) or (-1, -1)
-    _launch(cache, stream, lambda s: varlen_attn_fwd_paged(q, cu_seqlens_q, cache.batch, total_q, H, max_seqlen_q,
-                                                           cache.struct, scale, left, right, out, lse, workspace,
-                                                           workspace.numel() * workspace.element_size(), s),
-            "varlen_attn_fwd_paged", *fresh)
+    _paged_call(LIB.varlen_attn_fwd_paged, cache, stream, fresh,
+                (qp, qs, cu, cache.batch, total_q, H, max_seqlen_q, cache.ref, D ** -0.5 if scale is None else scale,
+                 left, right, op, os_, lse.data_ptr(), workspace.data_ptr(), nbytes))
     return out, lse

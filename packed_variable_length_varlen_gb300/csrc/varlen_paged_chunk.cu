@@ -46,12 +46,12 @@ struct ChunkCfg {
   static constexpr int NC = (D + 63) / 64;           // 64-column chunks of a bf16 tile
   static constexpr int CHUNK = 128 * 128;            // 128 rows x 128 bytes
   static constexpr int TILE = NC * CHUNK;            // one Q / K / V tile in bf16
-  static constexpr int NSLOT = E4M3 ? 3 : (NC == 1 ? 8 : 4);  // bf16 K/V ring (even for bf16: K and V slots alternate)
-  static constexpr int NRAW = E4M3 ? 3 : 0;          // ring of codes
+  static constexpr int NSLOT = E4M3 ? 4 : (NC == 1 ? 8 : 4);  // bf16 K/V ring (even for bf16: K and V slots alternate)
+  static constexpr int NRAW = E4M3 ? 2 : 0;          // ring of codes
   static constexpr int SCALES = 1024;                // page pieces of at least 16 keys, 128 bytes apart
   static constexpr int O_COL = 256;                  // TMEM column of O_A (O_B at +128)
   static constexpr int KSTEPS = D / 16;
-  static constexpr int SMEM = 2048 + TILE * (2 + NSLOT) + NRAW * (CHUNK + SCALES);
+  static constexpr int SMEM = 1024 + TILE * (2 + NSLOT) + NRAW * (CHUNK + SCALES);
   // Registers (threads x registers at launch is all there is to share out):
   // bf16 384 x 168 = 128 x (120 + 192 + 192); E4M3 512 x 128 = 128 x (72 + 184 + 184 + 72).
   static constexpr uint32_t REGS_LAUNCH = E4M3 ? 128 : 168, REGS_CTL = E4M3 ? 72 : 120, REGS_SOFTMAX = E4M3 ? 184 : 192,
@@ -65,14 +65,14 @@ struct ChunkShared {
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t mma_done;
   uint64_t kv_full[8], kv_empty[8], v_ok[8];
-  uint64_t raw_full[3], raw_empty[3];
+  uint64_t raw_full[2], raw_empty[2];
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint32_t tmem_base;
   int abort;
   PagedPiece piece[kPieces];
   PagedStart start;
 };
-static_assert(sizeof(ChunkShared) <= 2048, "barrier block too large");
+static_assert(sizeof(ChunkShared) <= 1024, "barrier block too large");
 
 // The next piece from the ring (b < 0: there is none); false on giving up.
 struct PieceReader {
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
     return;
   }
   ChunkShared& sh = *reinterpret_cast<ChunkShared*>(smem);
-  uint8_t* q_smem = smem + 2048;  // Q_A then Q_B
+  uint8_t* q_smem = smem + 1024;  // Q_A then Q_B
   uint8_t* ring = q_smem + 2 * C::TILE;
   uint8_t* raw = ring + C::NSLOT * C::TILE;          // codes
   uint8_t* scales = raw + C::NRAW * C::CHUNK;
@@ -491,11 +491,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
   } else if constexpr (E4M3) {
     warpgroup_set_regs<C::REGS_CONVERT, C::REGS_LAUNCH>();
     // ------------------------------------------------------------ codes to bf16
-    // Eight lanes take a key's 128 bytes of codes, 16 each: 32 bytes of bf16 in
-    // two 16-byte stores.  The lanes of the second column chunk store their
-    // halves the other way round, so that eight lanes meet eight bank groups.
+    // A thread takes the 64 codes of one column chunk of a key (64 threads walk
+    // down one chunk, so that eight lanes meet eight bank groups in reading and
+    // in writing): the key's scale is looked up once for all of them.
     const int t = threadIdx.x - 384;  // 0..127
-    const int q = t & 7, r0 = t >> 3;
+    const int cc = C::NC == 2 ? t >> 6 : 0, r0 = C::NC == 2 ? t & 63 : t;
     const int box_shift = min(p.pages.page_shift, 7);
     PieceReader pieces;
     PagedPiece x;
@@ -516,40 +516,39 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
           uint8_t* dst = ring + s * C::TILE;
           // rows of V that no row of the unit sees may hold anything: cleared
           const int lo = which ? x.u.lo - key0 : -1, hi = which ? x.u.hi - key0 : kChunkTile;
-#pragma unroll 4
-          for (int i = 0; i < 8; ++i) {
-            const int r = r0 + i * 16;
-            const uint4 u = *reinterpret_cast<const uint4*>(src + r * 128 + ((q ^ (r & 7)) << 4));
+#pragma unroll
+          for (int i = 0; i < C::NC; ++i) {
+            const int r = r0 + i * 64;
             const float f = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
                 sc + ((r >> box_shift) << 7) + ((r & ((1 << box_shift) - 1)) << 1)));
-            const bool large = f > 0x1p7f;  // 2^120 * scale does not fit into bf16: in two factors
-            const float f1 = large ? 0x1p127f : f * 0x1p120f;
+            const bool keep = r >= lo && r < hi, large = keep && f > 0x1p7f;
+            // 2^120 * scale, 0 for a row to clear (the codes' bits are finite in any case)
+            const float f1 = keep ? (large ? 0x1p127f : f * 0x1p120f) : 0.f;
             const uint32_t ff = pack_bf16x2(f1, f1);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-            uint32_t y[8];
+            const uint8_t* from = src + r * 128;
+            uint8_t* to = dst + cc * C::CHUNK + r * 128;
+            uint4 u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[k] = *reinterpret_cast<const uint4*>(from + (((cc * 4 + k) ^ (r & 7)) << 4));
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              y[2 * k] = mul_pair(raw_pair(__byte_perm(w[k], 0, 0x1000)), ff);
-              y[2 * k + 1] = mul_pair(raw_pair(__byte_perm(w[k], 0, 0x3020)), ff);
-            }
-            if (__any_sync(0xffffffffu, large)) {
-              const float f2 = large ? f * 0x1p-7f : 1.f;
-              const uint32_t gg = pack_bf16x2(f2, f2);
+              const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+              uint32_t y[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) y[k] = mul_pair(y[k], gg);
+              for (int e = 0; e < 4; ++e) {
+                y[2 * e] = mul_pair(raw_pair(__byte_perm(w[e], 0, 0x1000)), ff);
+                y[2 * e + 1] = mul_pair(raw_pair(__byte_perm(w[e], 0, 0x3020)), ff);
+              }
+              *reinterpret_cast<uint4*>(to + (((2 * k) ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(to + (((2 * k + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
             }
-            const bool keep = r >= lo && r < hi;
-            if (!keep) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) y[k] = 0u;
-            }
-            const int cc = q >> 2, sub = (q & 3) * 2;
-            if (cc < C::NC) {
-              uint8_t* row = dst + cc * C::CHUNK + r * 128;
-              const uint4 first = cc ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
-              const uint4 second = cc ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(y[4], y[5], y[6], y[7]);
-              *reinterpret_cast<uint4*>(row + (((sub + cc) ^ (r & 7)) << 4)) = first;
-              *reinterpret_cast<uint4*>(row + (((sub + 1 - cc) ^ (r & 7)) << 4)) = second;
+            if (large) {  // 2^120 * scale does not fit into a bf16: times the rest of it
+              const uint32_t gg = pack_bf16x2(f * 0x1p-7f, f * 0x1p-7f);
+#pragma unroll 1
+              for (int k = 0; k < 32; ++k) {
+                uint32_t* y = reinterpret_cast<uint32_t*>(to) + k;
+                *y = mul_pair(*y, gg);
+              }
             }
           }
           fence_proxy_async_smem();

@@ -12,11 +12,63 @@ namespace {
 // (blockIdx.x; most have none), its rows shared out over blockIdx.y.  With
 // parts i in the order of the CTAs: m = max m_i, w_i = 2^(m_i - m), l = sum l_i
 // w_i, O = sum w_i o_i / l.  The weights come first, so that the loads of o
-// depend on nothing: a unit of 228 parts takes 5 us where a running maximum
-// over them took 19.  The warps take every kJoinWarps-th part, and their sums
-// are added in the order of the warps.
-constexpr int kJoinWarps = 8, kJoinRows = 8;
+// depend on nothing (a unit of 228 parts takes 5 us where a running maximum
+// over them took 19).  A warp takes a row; where a unit of few rows has more
+// than kWarpParts parts, a block does, its warps every kJoinWarps-th part, and
+// adds the sums of the warps in their order.
+constexpr int kJoinWarps = 8, kWarpParts = 16;
 constexpr int kMaxParts = few_ctas(true) * kMaxSms;
+
+struct JoinRow {
+  int64_t q;      // packed query row
+  int32_t head;
+};
+
+__device__ __forceinline__ void join_lse(const PagedParams& p, const JoinRow& r, float m, float l) {
+  float* la = p.lse + (int64_t)r.head * p.total_q + r.q;
+  if (in_span(p.lse_span, la, 4, p.err)) *la = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+}
+__device__ __forceinline__ float join_inv(float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); }  // no key: 0; NaN stays
+
+// One warp joins slot row `row` of the unit that CTA blockIdx.x began.
+template <int D>
+__device__ __forceinline__ void join_by_warp(const PagedParams& p, const PagedParts& parts, const PagedJoin& u,
+                                             int32_t row, const JoinRow& r, float* weight) {
+  const int lane = threadIdx.x & 31;
+  auto at = [&](int32_t k) { return (2 * ((int64_t)blockIdx.x + k) + (k == 0 ? 1 : 0)) * parts.rows + row; };
+  float m = -INFINITY, l = 0.f;
+  for (int32_t k = lane; k < u.parts; k += 32) {
+    const float2 ml = *reinterpret_cast<const float2*>(parts.ml + at(k) * 2);
+    weight[2 * k] = ml.x;
+    weight[2 * k + 1] = ml.y;
+    m = fmaxf(m, ml.x);
+  }
+#pragma unroll
+  for (int w = 16; w >= 1; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+  const float ref = m == -INFINITY ? 0.f : m;
+  for (int32_t k = lane; k < u.parts; k += 32) {
+    weight[2 * k] = ex2(weight[2 * k] - ref);
+    l += weight[2 * k + 1] * weight[2 * k];
+  }
+#pragma unroll
+  for (int w = 16; w >= 1; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+  __syncwarp();
+  float o[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+#pragma unroll 4
+  for (int32_t k = 0; k < u.parts; ++k) {
+    const float* oa = parts.o + at(k) * D + lane;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = fmaf(oa[i * 32], weight[2 * k], o[i]);
+  }
+  const float inv = join_inv(l);
+  __nv_bfloat16* a = p.out + r.q * p.o_rs + (int64_t)r.head * p.o_hs + lane;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+    if (in_span(p.out_span, a + i * 32, 2, p.err)) a[i * 32] = __float2bfloat16_rn(o[i] * inv);
+  if (lane == 0) join_lse(p, r, m, l);
+}
 
 // The sum (or maximum) of v over the block, in a fixed order.
 template <bool MAX>
@@ -37,7 +89,7 @@ __device__ __forceinline__ float block_reduce(float v, float* tmp) {
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     varlen_paged_join_kernel(const PagedParams p, const PagedParts parts) {
-  __shared__ float so[kJoinWarps][D], weight[kMaxParts], tmp[kJoinWarps];
+  __shared__ float so[kJoinWarps][D], weight[2 * kMaxParts], tmp[kJoinWarps];
   dependency_wait();
   const PagedJoin u = parts.join[blockIdx.x];
   dependents_may_launch();
@@ -46,19 +98,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int32_t q0 = clamp_row(__ldg(p.cu_q + u.b), p.total_q), q1 = clamp_row(__ldg(p.cu_q + u.b + 1), p.total_q);
   const int64_t first = (int64_t)u.blk * parts.unit_rows;
   const int32_t rows = (int32_t)min((int64_t)(q1 - q0) * p.group - first, (int64_t)parts.unit_rows);
-  for (int32_t row = blockIdx.y; row < rows; row += kJoinRows) {
+  auto row_of = [&](int32_t row) {
+    const int64_t r = first + row, tok = r / p.group;
+    return JoinRow{q0 + tok, u.kh * p.group + (int32_t)(r - tok * p.group)};
+  };
+  if (u.parts <= kWarpParts) {
+    const int32_t row = warp * gridDim.y + blockIdx.y;
+    if (row < rows) join_by_warp<D>(p, parts, u, row, row_of(row), weight + warp * 2 * kWarpParts);
+    return;
+  }
+  for (int32_t row = blockIdx.y; row < rows; row += gridDim.y) {
     auto at = [&](int32_t k) { return (2 * ((int64_t)blockIdx.x + k) + (k == 0 ? 1 : 0)) * parts.rows + row; };
     float m = -INFINITY;
     for (int32_t k = threadIdx.x; k < u.parts; k += kJoinWarps * 32) {
-      weight[k] = parts.ml[at(k) * 2];
-      m = fmaxf(m, weight[k]);
+      const float2 ml = *reinterpret_cast<const float2*>(parts.ml + at(k) * 2);
+      weight[2 * k] = ml.x;
+      weight[2 * k + 1] = ml.y;
+      m = fmaxf(m, ml.x);
     }
     m = block_reduce<true>(m, tmp);
     const float ref = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     for (int32_t k = threadIdx.x; k < u.parts; k += kJoinWarps * 32) {
-      weight[k] = ex2(weight[k] - ref);
-      l += parts.ml[at(k) * 2 + 1] * weight[k];
+      weight[2 * k] = ex2(weight[2 * k] - ref);
+      l += weight[2 * k + 1] * weight[2 * k];
     }
     l = block_reduce<false>(l, tmp);  // (and the weights are there)
     float o[D / 32];
@@ -68,92 +131,51 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     for (int32_t k = warp; k < u.parts; k += kJoinWarps) {
       const float* oa = parts.o + at(k) * D + lane;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(oa[i * 32], weight[k], o[i]);
+      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(oa[i * 32], weight[2 * k], o[i]);
     }
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) so[warp][i * 32 + lane] = o[i];
     __syncthreads();
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no key: 0; NaN stays
-    const int64_t r = first + row;
-    const int32_t tok = (int32_t)(r / p.group), hd = u.kh * p.group + (int32_t)(r - (int64_t)tok * p.group);
+    const JoinRow r = row_of(row);
     if (threadIdx.x < D) {
       float x = 0.f;
       for (int w = 0; w < kJoinWarps; ++w) x += so[w][threadIdx.x];
-      __nv_bfloat16* a = p.out + (int64_t)(q0 + tok) * p.o_rs + (int64_t)hd * p.o_hs + threadIdx.x;
-      if (in_span(p.out_span, a, 2, p.err)) *a = __float2bfloat16_rn(x * inv);
+      __nv_bfloat16* a = p.out + r.q * p.o_rs + (int64_t)r.head * p.o_hs + threadIdx.x;
+      if (in_span(p.out_span, a, 2, p.err)) *a = __float2bfloat16_rn(x * join_inv(l));
     }
-    if (threadIdx.x == 0) {
-      float* la = p.lse + (int64_t)hd * p.total_q + q0 + tok;
-      if (in_span(p.lse_span, la, 4, p.err)) *la = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
-    }
+    if (threadIdx.x == 0) join_lse(p, r, m, l);
     __syncthreads();
   }
 }
 
-// The same for the kernel for many rows, whose units have 256 rows and mostly
-// few parts: a warp takes a row.
+// The same for the kernel for many rows, whose units have 256 rows: one row a
+// warp, kChunkRows / kJoinWarps blocks a unit.
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     varlen_paged_join_rows_kernel(const PagedParams p, const PagedParts parts) {
-  __shared__ float weights[kJoinWarps][kMaxSms];
+  __shared__ float weight[kJoinWarps][2 * kMaxSms];
   dependency_wait();
   const PagedJoin u = parts.join[blockIdx.x];
   dependents_may_launch();
   if (u.parts == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* weight = weights[warp];
+  const int32_t warp = threadIdx.x >> 5, row = blockIdx.y * kJoinWarps + warp;
   const int32_t q0 = clamp_row(__ldg(p.cu_q + u.b), p.total_q), q1 = clamp_row(__ldg(p.cu_q + u.b + 1), p.total_q);
   const int32_t half_tokens = kChunkRows / 2 / p.group;
-  for (int32_t row = blockIdx.y * kJoinWarps + warp; row < kChunkRows; row += gridDim.y * kJoinWarps) {
-    const int32_t half = row >> 7, in_half = row & 127, t = in_half / p.group;
-    const int64_t tok = (int64_t)u.blk * 2 * half_tokens + half * half_tokens + t;
-    if (t >= half_tokens || tok >= q1 - q0) continue;
-    auto at = [&](int32_t k) { return (2 * ((int64_t)blockIdx.x + k) + (k == 0 ? 1 : 0)) * parts.rows + row; };
-    float m = -INFINITY, l = 0.f;
-    for (int32_t k = lane; k < u.parts; k += 32) {
-      weight[k] = parts.ml[at(k) * 2];
-      m = fmaxf(m, weight[k]);
-    }
-#pragma unroll
-    for (int w = 16; w >= 1; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-    const float ref = m == -INFINITY ? 0.f : m;
-    for (int32_t k = lane; k < u.parts; k += 32) {
-      weight[k] = ex2(weight[k] - ref);
-      l += parts.ml[at(k) * 2 + 1] * weight[k];
-    }
-#pragma unroll
-    for (int w = 16; w >= 1; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-    __syncwarp();
-    float o[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-#pragma unroll 4
-    for (int32_t k = 0; k < u.parts; ++k) {
-      const float* oa = parts.o + at(k) * D + lane;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(oa[i * 32], weight[k], o[i]);
-    }
-    __syncwarp();
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    const int32_t hd = u.kh * p.group + in_half - t * p.group;
-    __nv_bfloat16* a = p.out + (q0 + tok) * p.o_rs + (int64_t)hd * p.o_hs + lane;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-      if (in_span(p.out_span, a + i * 32, 2, p.err)) a[i * 32] = __float2bfloat16_rn(o[i] * inv);
-    float* la = p.lse + (int64_t)hd * p.total_q + q0 + tok;
-    if (lane == 0 && in_span(p.lse_span, la, 4, p.err))
-      *la = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
-  }
+  const int32_t half = row >> 7, in_half = row & 127, t = in_half / p.group;
+  const int64_t tok = (int64_t)u.blk * 2 * half_tokens + half * half_tokens + t;
+  if (t >= half_tokens || tok >= q1 - q0) return;
+  join_by_warp<D>(p, parts, u, row, JoinRow{q0 + tok, u.kh * p.group + in_half - t * p.group}, weight[warp]);
 }
 
 template <int D>
 cudaError_t launch_join_d(const PagedLaunch& L, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (L.few)
-    e = launch_overlapped(varlen_paged_join_kernel<D>, dim3(L.sms * few_ctas(L.e4m3), kJoinRows), kJoinWarps * 32, 0,
-                          stream, L.p, L.few_parts);
+    e = launch_overlapped(varlen_paged_join_kernel<D>,
+                          dim3(L.sms * few_ctas(L.e4m3), L.few_parts.rows < kJoinWarps ? L.few_parts.rows : kJoinWarps),
+                          kJoinWarps * 32, 0, stream, L.p, L.few_parts);
   if (e == cudaSuccess && L.many)
-    e = launch_overlapped(varlen_paged_join_rows_kernel<D>, dim3(L.sms, 8), kJoinWarps * 32, 0, stream, L.p, L.chunk);
+    e = launch_overlapped(varlen_paged_join_rows_kernel<D>, dim3(L.sms, kChunkRows / kJoinWarps), kJoinWarps * 32, 0, stream, L.p, L.chunk);
   return e;
 }
 

@@ -396,7 +396,7 @@ int varlen_attn_cache_read(const varlen_kv_cache* cache, const int32_t* cu_seqle
  * Forward over the cache: packed queries q [total_q, num_heads, head_dim]
  * (bf16, cu_seqlens_q) against all seqlens[b] positions of their sequence.
  * num_heads is a multiple of the cache's num_kv_heads and at most 128 times
- * it (VARLEN_ERR_SHAPE); query head h reads key head
+ * it, total_q * num_heads below 2^31 - 256 (VARLEN_ERR_SHAPE); query head h reads key head
  * h / (num_heads / num_kv_heads).  The band, out and lse are those of
  * varlen_attn_fwd_window with Sk = seqlens[b]: (-1, -1) no mask, (-1, 0)
  * causal with the last query at the last key, so after

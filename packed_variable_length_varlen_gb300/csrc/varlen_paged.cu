@@ -8,15 +8,15 @@ namespace varlen {
 
 namespace {
 
-// One unit per CTA of the attention kernel that began but did not end one
-// (blockIdx.x; most have none), its rows shared out over blockIdx.y.  With
-// parts i in the order of the CTAs: m = max m_i, w_i = 2^(m_i - m), l = sum l_i
-// w_i, O = sum w_i o_i / l.  The weights come first, so that the loads of o
-// depend on nothing (a unit of 228 parts takes 5 us where a running maximum
-// over them took 19).  A warp takes a row; where a unit of few rows has more
-// than kWarpParts parts, a block does, its warps every kJoinWarps-th part, and
-// adds the sums of the warps in their order.
-constexpr int kJoinWarps = 8, kWarpParts = 16;
+// A block for each CTA of the attention kernel joins the unit that the CTA began
+// but did not end (most have none).  With parts i in the order of the CTAs: m =
+// max m_i, w_i = 2^(m_i - m), l = sum l_i w_i, O = sum w_i o_i / l.  The weights
+// come first, so that the loads of o depend on nothing.  A warp takes a row.
+// Where a unit has more than kWarpParts parts, the blocks of the CTAs that
+// hold it take a row each, its parts shared out over the warps, whose sums are
+// added in order: a unit of 228 parts and 8 rows takes FIG us (a running
+// maximum over the parts in one block took 19).
+constexpr int kJoinWarps = 16, kWarpParts = 16;
 constexpr int kMaxParts = few_ctas(true) * kMaxSms;
 
 struct JoinRow {
@@ -30,12 +30,12 @@ __device__ __forceinline__ void join_lse(const PagedParams& p, const JoinRow& r,
 }
 __device__ __forceinline__ float join_inv(float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); }  // no key: 0; NaN stays
 
-// One warp joins slot row `row` of the unit that CTA blockIdx.x began.
+// One warp joins slot row `row` of unit u.
 template <int D>
 __device__ __forceinline__ void join_by_warp(const PagedParams& p, const PagedParts& parts, const PagedJoin& u,
                                              int32_t row, const JoinRow& r, float* weight) {
   const int lane = threadIdx.x & 31;
-  auto at = [&](int32_t k) { return (2 * ((int64_t)blockIdx.x + k) + (k == 0 ? 1 : 0)) * parts.rows + row; };
+  auto at = [&](int32_t k) { return (2 * (int64_t)(u.first + k) + (k == 0 ? 1 : 0)) * parts.rows + row; };
   float m = -INFINITY, l = 0.f;
   for (int32_t k = lane; k < u.parts; k += 32) {
     const float2 ml = *reinterpret_cast<const float2*>(parts.ml + at(k) * 2);
@@ -86,79 +86,92 @@ __device__ __forceinline__ float block_reduce(float v, float* tmp) {
   return v;
 }
 
+// The whole block joins row `row` of unit u.
+template <int D>
+__device__ __forceinline__ void join_by_block(const PagedParams& p, const PagedParts& parts, const PagedJoin& u,
+                                              int32_t row, const JoinRow& r, float* weight, float (*so)[D], float* tmp) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto at = [&](int32_t k) { return (2 * (int64_t)(u.first + k) + (k == 0 ? 1 : 0)) * parts.rows + row; };
+  float m = -INFINITY;
+  for (int32_t k = threadIdx.x; k < u.parts; k += kJoinWarps * 32) {
+    const float2 ml = *reinterpret_cast<const float2*>(parts.ml + at(k) * 2);
+    weight[2 * k] = ml.x;
+    weight[2 * k + 1] = ml.y;
+    m = fmaxf(m, ml.x);
+  }
+  m = block_reduce<true>(m, tmp);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  for (int32_t k = threadIdx.x; k < u.parts; k += kJoinWarps * 32) {
+    weight[2 * k] = ex2(weight[2 * k] - ref);
+    l += weight[2 * k + 1] * weight[2 * k];
+  }
+  l = block_reduce<false>(l, tmp);  // (and the weights are there)
+  float o[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+#pragma unroll 8
+  for (int32_t k = warp; k < u.parts; k += kJoinWarps) {
+    const float* oa = parts.o + at(k) * D + lane;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = fmaf(oa[i * 32], weight[2 * k], o[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) so[warp][i * 32 + lane] = o[i];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float x = 0.f;
+    for (int w = 0; w < kJoinWarps; ++w) x += so[w][threadIdx.x];
+    __nv_bfloat16* a = p.out + r.q * p.o_rs + (int64_t)r.head * p.o_hs + threadIdx.x;
+    if (in_span(p.out_span, a, 2, p.err)) *a = __float2bfloat16_rn(x * join_inv(l));
+  }
+  if (threadIdx.x == 0) join_lse(p, r, m, l);
+  __syncthreads();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     varlen_paged_join_kernel(const PagedParams p, const PagedParts parts) {
   __shared__ float so[kJoinWarps][D], weight[2 * kMaxParts], tmp[kJoinWarps];
   dependency_wait();
-  const PagedJoin u = parts.join[blockIdx.x];
+  const PagedJoin units[2] = {parts.join[2 * blockIdx.x], parts.join[2 * blockIdx.x + 1]};
   dependents_may_launch();
-  if (u.parts == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t q0 = clamp_row(__ldg(p.cu_q + u.b), p.total_q), q1 = clamp_row(__ldg(p.cu_q + u.b + 1), p.total_q);
-  const int64_t first = (int64_t)u.blk * parts.unit_rows;
-  const int32_t rows = (int32_t)min((int64_t)(q1 - q0) * p.group - first, (int64_t)parts.unit_rows);
-  auto row_of = [&](int32_t row) {
-    const int64_t r = first + row, tok = r / p.group;
-    return JoinRow{q0 + tok, u.kh * p.group + (int32_t)(r - tok * p.group)};
-  };
-  if (u.parts <= kWarpParts) {
-    const int32_t row = warp * gridDim.y + blockIdx.y;
-    if (row < rows) join_by_warp<D>(p, parts, u, row, row_of(row), weight + warp * 2 * kWarpParts);
-    return;
-  }
-  for (int32_t row = blockIdx.y; row < rows; row += gridDim.y) {
-    auto at = [&](int32_t k) { return (2 * ((int64_t)blockIdx.x + k) + (k == 0 ? 1 : 0)) * parts.rows + row; };
-    float m = -INFINITY;
-    for (int32_t k = threadIdx.x; k < u.parts; k += kJoinWarps * 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(parts.ml + at(k) * 2);
-      weight[2 * k] = ml.x;
-      weight[2 * k + 1] = ml.y;
-      m = fmaxf(m, ml.x);
+  const int warp = threadIdx.x >> 5;
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const PagedJoin u = units[which];
+    if (u.parts == 0 || (which == 0 && u.parts <= kWarpParts)) continue;  // block-uniform
+    const int32_t q0 = clamp_row(__ldg(p.cu_q + u.b), p.total_q), q1 = clamp_row(__ldg(p.cu_q + u.b + 1), p.total_q);
+    const int32_t first = u.blk * kFewRows, rows = min((q1 - q0) * p.group - first, kFewRows);
+    auto row_of = [&](int32_t row) {
+      const int32_t tok = (first + row) / p.group;
+      return JoinRow{(int64_t)q0 + tok, u.kh * p.group + first + row - tok * p.group};
+    };
+    if (u.parts <= kWarpParts) {
+      for (int32_t row = warp; row < rows; row += kJoinWarps)
+        join_by_warp<D>(p, parts, u, row, row_of(row), weight + warp * 2 * kWarpParts);
+    } else {
+      const int32_t blocks = min(u.parts, rows);  // that share the rows
+      for (int32_t row = blockIdx.x - u.first; row < rows && (int32_t)blockIdx.x - u.first < blocks; row += blocks)
+        join_by_block<D>(p, parts, u, row, row_of(row), weight, so, tmp);
     }
-    m = block_reduce<true>(m, tmp);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int32_t k = threadIdx.x; k < u.parts; k += kJoinWarps * 32) {
-      weight[2 * k] = ex2(weight[2 * k] - ref);
-      l += weight[2 * k + 1] * weight[2 * k];
-    }
-    l = block_reduce<false>(l, tmp);  // (and the weights are there)
-    float o[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-#pragma unroll 8
-    for (int32_t k = warp; k < u.parts; k += kJoinWarps) {
-      const float* oa = parts.o + at(k) * D + lane;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(oa[i * 32], weight[2 * k], o[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) so[warp][i * 32 + lane] = o[i];
-    __syncthreads();
-    const JoinRow r = row_of(row);
-    if (threadIdx.x < D) {
-      float x = 0.f;
-      for (int w = 0; w < kJoinWarps; ++w) x += so[w][threadIdx.x];
-      __nv_bfloat16* a = p.out + r.q * p.o_rs + (int64_t)r.head * p.o_hs + threadIdx.x;
-      if (in_span(p.out_span, a, 2, p.err)) *a = __float2bfloat16_rn(x * join_inv(l));
-    }
-    if (threadIdx.x == 0) join_lse(p, r, m, l);
     __syncthreads();
   }
 }
 
-// The same for the kernel for many rows, whose units have 256 rows: one row a
-// warp, kChunkRows / kJoinWarps blocks a unit.
+// The same for the kernel for many rows, whose units have 256 rows: a row a
+// warp, kChunkRows / kRowsWarps blocks a unit.
+constexpr int kRowsWarps = 8;
+
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32)
+__global__ void __launch_bounds__(kRowsWarps * 32)
     varlen_paged_join_rows_kernel(const PagedParams p, const PagedParts parts) {
-  __shared__ float weight[kJoinWarps][2 * kMaxSms];
+  __shared__ float weight[kRowsWarps][2 * kMaxSms];
   dependency_wait();
-  const PagedJoin u = parts.join[blockIdx.x];
+  const PagedJoin u = parts.join[2 * blockIdx.x + 1];
   dependents_may_launch();
   if (u.parts == 0) return;
-  const int32_t warp = threadIdx.x >> 5, row = blockIdx.y * kJoinWarps + warp;
+  const int32_t warp = threadIdx.x >> 5, row = blockIdx.y * kRowsWarps + warp;
   const int32_t q0 = clamp_row(__ldg(p.cu_q + u.b), p.total_q), q1 = clamp_row(__ldg(p.cu_q + u.b + 1), p.total_q);
   const int32_t half_tokens = kChunkRows / 2 / p.group;
   const int32_t half = row >> 7, in_half = row & 127, t = in_half / p.group;
@@ -172,10 +185,9 @@ cudaError_t launch_join_d(const PagedLaunch& L, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (L.few)
     e = launch_overlapped(varlen_paged_join_kernel<D>,
-                          dim3(L.sms * few_ctas(L.e4m3), L.few_parts.rows < kJoinWarps ? L.few_parts.rows : kJoinWarps),
-                          kJoinWarps * 32, 0, stream, L.p, L.few_parts);
+                          dim3(L.sms * few_ctas(L.e4m3)), kJoinWarps * 32, 0, stream, L.p, L.few_parts);
   if (e == cudaSuccess && L.many)
-    e = launch_overlapped(varlen_paged_join_rows_kernel<D>, dim3(L.sms, kChunkRows / kJoinWarps), kJoinWarps * 32, 0, stream, L.p, L.chunk);
+    e = launch_overlapped(varlen_paged_join_rows_kernel<D>, dim3(L.sms, kChunkRows / kRowsWarps), kRowsWarps * 32, 0, stream, L.p, L.chunk);
   return e;
 }
 

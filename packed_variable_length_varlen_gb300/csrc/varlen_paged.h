@@ -114,10 +114,11 @@ constexpr int kChunkRows = 256;   // rows of a unit of the kernel for many rows 
 constexpr int kChunkTile = 128;   // keys per tile of that kernel
 constexpr int kMaxSms = 160;      // the workspace is sized for this many
 
-// What CTA c left for the join: the unit that it begins and does not end, and
-// the number of CTAs that hold it (0: none).
+// What CTA c left for the join: [2 c + 1] the unit that it begins and does not
+// end, [2 c] the unit that an earlier CTA began: the CTA that began it and the
+// number of CTAs that hold it (0: there is no such unit).
 struct PagedJoin {
-  int32_t b, kh, blk, parts;
+  int32_t b, kh, blk, first, parts;
 };
 
 // Partial results of one kernel in the workspace: slot 2 c + (the CTA begins
@@ -127,8 +128,7 @@ struct PagedParts {
   float* o;
   float* ml;
   PagedJoin* join;
-  int32_t rows;       // rows of a slot
-  int32_t unit_rows;  // rows of a unit
+  int32_t rows;  // rows of a slot
 };
 
 struct PagedLaunch {
@@ -160,10 +160,10 @@ inline PagedWorkspace paged_workspace(int64_t total_rows, int32_t head_dim) {
   const size_t few = (size_t)few_ctas(true) * kMaxSms, many = total_rows > kFewRows ? kMaxSms : 0;
   w.few_o = take(2 * few * w.few_rows * head_dim * 4);
   w.few_ml = take(2 * few * w.few_rows * 8);
-  w.few_join = take(few * sizeof(PagedJoin));
+  w.few_join = take(2 * few * sizeof(PagedJoin));
   w.chunk_o = take(2 * many * kChunkRows * head_dim * 4);
   w.chunk_ml = take(2 * many * kChunkRows * 8);
-  w.chunk_join = take(many * sizeof(PagedJoin));
+  w.chunk_join = take(2 * many * sizeof(PagedJoin));
   w.bytes = at;
   return w;
 }

@@ -2,6 +2,7 @@
 // attention over it (declared in varlen_attn.h): argument checks, 64-bit
 // extents, launches.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstring>
 #include <utility>
@@ -193,6 +194,7 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   const varlen_kv_cache& c = *cache;
   if (total_q < 0 || num_heads < 1 || num_heads % c.num_kv_heads != 0 || num_heads / c.num_kv_heads > 128)
     return VARLEN_ERR_SHAPE;
+  if ((int64_t)total_q * num_heads > INT32_MAX - 256) return VARLEN_ERR_SHAPE;  // rows are counted in 32 bits
   if (!(scale > 0.f) || !std::isfinite(scale)) return VARLEN_ERR_SHAPE;
   if (cu_seqlens_q == nullptr) return VARLEN_ERR_NULL;
   if ((st = check_nhd(q, sq, total_q, num_heads, c.head_dim, false)) != VARLEN_OK) return st;
@@ -256,9 +258,9 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   char* ws = static_cast<char*>(workspace);
   const PagedWorkspace w = paged_workspace(total_rows, c.head_dim);
   L.few_parts = PagedParts{reinterpret_cast<float*>(ws + w.few_o), reinterpret_cast<float*>(ws + w.few_ml),
-                           reinterpret_cast<PagedJoin*>(ws + w.few_join), w.few_rows, kFewRows};
+                           reinterpret_cast<PagedJoin*>(ws + w.few_join), w.few_rows};
   L.chunk = PagedParts{reinterpret_cast<float*>(ws + w.chunk_o), reinterpret_cast<float*>(ws + w.chunk_ml),
-                       reinterpret_cast<PagedJoin*>(ws + w.chunk_join), kChunkRows, kChunkRows};
+                       reinterpret_cast<PagedJoin*>(ws + w.chunk_join), kChunkRows};
   auto maps = [&](CUtensorMap* k, CUtensorMap* v, CUtensorMap* ks, CUtensorMap* vs, int tile) {
     const int box = std::min(c.page_size, tile);
     int s2;

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       if (lane == 0) {
-        parts.join[blockIdx.x].parts = 0;
+        parts.join[2 * blockIdx.x].parts = parts.join[2 * blockIdx.x + 1].parts = 0;
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
   if (warp == C::WARPS) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      parts.join[blockIdx.x].parts = 0;
+      parts.join[2 * blockIdx.x].parts = parts.join[2 * blockIdx.x + 1].parts = 0;
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
@@ -240,8 +240,8 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
     walk.init(sh.start, p, take);
     while (ok && walk.next(p, x)) {
       // rows of the unit: first is row `skip` of token t0
-      const int32_t skip = (int32_t)((int64_t)x.blk * kFewRows - (int64_t)x.u.t0 * p.group);
-      const int32_t rows = min((x.n - x.u.t0) * (int64_t)p.group - skip, (int64_t)kFewRows);
+      const int32_t skip = x.blk * kFewRows - x.u.t0 * p.group;
+      const int32_t rows = min((x.n - x.u.t0) * p.group - skip, kFewRows);
       const int mt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);  // row tiles
       const int rt = warp & (mt - 1), kg = warp / mt, share = C::WARPS / mt;
       const bool works = rt * 8 < rows;

@@ -43,8 +43,8 @@ struct PagedGeom {
   static constexpr int kRows = ROWS, kTile = TILE;
   __device__ static __forceinline__ int32_t half_tokens(const PagedParams& p) { return ROWS / 2 / p.group; }
   __device__ static __forceinline__ int32_t blocks(const PagedParams& p, int32_t n) {
-    if (BY_TOKEN) return (int32_t)(((int64_t)n + 2 * half_tokens(p) - 1) / (2 * half_tokens(p)));
-    return (int32_t)(((int64_t)n * p.group + ROWS - 1) / ROWS);
+    const uint32_t rows = BY_TOKEN ? n : n * p.group, per = BY_TOKEN ? 2 * half_tokens(p) : ROWS;
+    return (int32_t)((rows + per - 1) / per);
   }
   __device__ static __forceinline__ PagedUnit unit(const PagedParams& p, int32_t n, int32_t sk, int32_t blk) {
     PagedUnit u;
@@ -53,9 +53,9 @@ struct PagedGeom {
       u.t0 = blk * bt;
       u.t1 = min(n - u.t0, bt) + u.t0 - 1;
     } else {
-      const int64_t r0 = (int64_t)blk * ROWS, r1 = min((int64_t)n * p.group, r0 + ROWS) - 1;
-      u.t0 = (int32_t)(r0 / p.group);
-      u.t1 = (int32_t)(r1 / p.group);
+      const uint32_t r0 = (uint32_t)blk * ROWS, r1 = min((uint32_t)(n * p.group), r0 + ROWS) - 1;
+      u.t0 = (int32_t)(r0 / (uint32_t)p.group);
+      u.t1 = (int32_t)(r1 / (uint32_t)p.group);
     }
     band_keys(u.t0, u.t1, n, sk, p.win_left, p.win_right, &u.lo, &u.hi);
     u.tile0 = u.lo / TILE;
@@ -71,7 +71,7 @@ __device__ __forceinline__ PagedSeg paged_seg(const PagedParams& p, int32_t b, i
   s.q0 = a;
   s.n = max(e - a, 0);
   s.sk = cache_len(p.pages, b);
-  const bool few = (int64_t)s.n * p.group <= kFewRows;
+  const bool few = s.n * p.group <= kFewRows;  // (total_q * num_heads < 2^31)
   if ((take == kTakeFew && !few) || (take == kTakeMany && few)) s.n = 0;
   s.blocks = G::blocks(p, s.n);
   s.per_head = 0;
@@ -97,24 +97,35 @@ struct PagedStart {
   int64_t total, first, count;  // tiles of the launch; first tile and number of tiles of this CTA
   int64_t off;                  // first tile's place within segment b
   int32_t b, ctas;              // segment; CTAs that have work
-  long long sums[32];
+  PagedSeg seg;                 // of segment b
+  long long sums[16];
 };
+
+// n / d: 64-bit division is a long subroutine, and hardly ever needed here.
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  if (((uint64_t)n | (uint64_t)d) >> 32 == 0) return (int64_t)((uint32_t)n / (uint32_t)d);
+  return n / d;
+}
 
 // CTAs that share `total` tiles: no more than leave each `least`.
 __device__ __forceinline__ int32_t paged_ctas(int64_t total, int32_t grid, int32_t least) {
-  const int64_t n = (total + least - 1) / least;
+  const int64_t n = quotient(total + least - 1, least);
   return (int32_t)(n < 1 ? 1 : (n < grid ? n : grid));
 }
-// (total * c cannot overflow: fewer than 2^31 tokens of 2^7 rows over 2^31
-// keys would take years; any launch that ends has total < 2^50, c < 2^10)
-__device__ __forceinline__ int64_t paged_first(int64_t total, int32_t ctas, int32_t c) { return total * c / ctas; }
-// The CTA that has tile x.
-__device__ __forceinline__ int32_t paged_owner(int64_t total, int32_t ctas, int64_t x) {
-  int32_t c = (int32_t)(x * ctas / total);
-  while (c + 1 < ctas && paged_first(total, ctas, c + 1) <= x) ++c;
-  while (c > 0 && paged_first(total, ctas, c) > x) --c;
-  return c;
-}
+// First tile of CTA c: the parts have total / ctas tiles, the first total %
+// ctas of them one more.
+struct PagedShares {
+  int64_t each, more;
+  __device__ __forceinline__ PagedShares(int64_t total, int32_t ctas) {
+    each = quotient(total, ctas);
+    more = total - each * ctas;
+  }
+  __device__ __forceinline__ int64_t first(int32_t c) const { return each * c + min((int64_t)c, more); }
+  __device__ __forceinline__ int32_t owner(int64_t x) const {
+    const int64_t big = more * (each + 1);
+    return (int32_t)(x < big ? quotient(x, each + 1) : more + quotient(x - big, each));
+  }
+};
 
 __device__ __forceinline__ long long warp_inclusive(long long v) {
 #pragma unroll
@@ -126,51 +137,69 @@ __device__ __forceinline__ long long warp_inclusive(long long v) {
 }
 
 // Fills `st` (shared memory).  Every thread of the CTA (a whole number of
-// warps) calls it; the CTA is synchronised when it returns.
+// warps, at most 16) calls it; the CTA is synchronised when it returns.
 template <class G>
 __device__ __forceinline__ void paged_start(PagedStart& st, const PagedParams& p, int32_t take, int32_t least) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  long long mine = 0, mine_first = 0;
+  // batches of at most a thread's segment each are scanned once; larger ones
+  // are summed first and then searched
+  const bool one = p.batch <= (int32_t)blockDim.x;
+  PagedSeg seg;
+  seg.per_head = 0;
+  long long mine = 0;
   for (int32_t b = threadIdx.x; b < p.batch; b += blockDim.x) {
-    const long long c = (long long)p.kv_heads * paged_seg<G>(p, b, take).per_head;
-    if (b < (int)blockDim.x) mine_first = c;
-    mine += c;
+    seg = paged_seg<G>(p, b, take);
+    mine += (long long)p.kv_heads * seg.per_head;
   }
   long long incl = warp_inclusive(mine);
   if (lane == 31) st.sums[warp] = incl;
+  if (threadIdx.x == 0) st.b = st.off = 0;
   __syncthreads();
-  long long total = 0;
-  for (int w = 0; w < warps; ++w) total += st.sums[w];
+  long long total = 0, excl = incl - mine;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) excl += st.sums[w];
+    total += st.sums[w];
+  }
   const int32_t ctas = paged_ctas(total, gridDim.x, least);
   const bool works = total > 0 && (int32_t)blockIdx.x < ctas;
-  const int64_t first = works ? paged_first(total, ctas, blockIdx.x) : 0;
-  const int64_t last = works ? paged_first(total, ctas, blockIdx.x + 1) : 0;
+  const PagedShares shares(total, ctas);
+  const int64_t first = works ? shares.first(blockIdx.x) : 0;
   if (threadIdx.x == 0) {
     st.total = total;
     st.ctas = ctas;
     st.first = first;
-    st.count = last - first;
-    st.off = 0;
-    st.b = 0;
+    st.count = works ? shares.first(blockIdx.x + 1) - first : 0;
+  }
+  if (one || !works) {  // CTA-uniform
+    if (works && first >= excl && first < excl + mine) {
+      st.b = threadIdx.x;
+      st.off = first - excl;
+      st.seg = seg;
+    }
+    __syncthreads();
+    return;
   }
   __syncthreads();
-  if (!works) return;  // CTA-uniform
   long long before = 0;
   for (int32_t base = 0; base < p.batch; base += blockDim.x) {
     const int32_t b = base + threadIdx.x;
-    const long long c =
-        b >= p.batch ? 0 : (base == 0 ? mine_first : (long long)p.kv_heads * paged_seg<G>(p, b, take).per_head);
+    long long c = 0;
+    if (b < p.batch) {
+      seg = paged_seg<G>(p, b, take);
+      c = (long long)p.kv_heads * seg.per_head;
+    }
     incl = warp_inclusive(c);
     if (lane == 31) st.sums[warp] = incl;
     __syncthreads();
-    long long excl = before + incl - c, all = 0;
+    long long e = before + incl - c, all = 0;
     for (int w = 0; w < warps; ++w) {
-      if (w < warp) excl += st.sums[w];
+      if (w < warp) e += st.sums[w];
       all += st.sums[w];
     }
-    if (first >= excl && first < excl + c) {
+    if (first >= e && first < e + c) {
       st.b = b;
-      st.off = first - excl;
+      st.off = first - e;
+      st.seg = seg;
     }
     before += all;
     __syncthreads();
@@ -190,9 +219,9 @@ struct PagedWalk {
     b = st.b;
     kh = blk = j = 0;
     if (left <= 0) return;
-    s = paged_seg<G>(p, b, take);
+    s = st.seg;
     int64_t off = st.off;
-    kh = (int32_t)(off / s.per_head);
+    kh = (int32_t)quotient(off, s.per_head);
     off -= (int64_t)kh * s.per_head;
     while (true) {
       const int32_t c = max(G::unit(p, s.n, s.sk, blk).tiles, 1);
@@ -237,12 +266,16 @@ struct PagedWalk {
 };
 
 // Left for the join by the one thread that calls it, for every piece: the
-// unit that the CTA begins and does not end (its last piece, if any).
+// units that the CTA holds a part of (its first and its last piece, if any).
 __device__ __forceinline__ void paged_note(PagedJoin* join, const PagedStart& st, const PagedPiece& x) {
-  if (!x.begins() || x.ends()) return;
-  const int64_t end = st.first + st.count + (x.cost - x.j1) - 1;  // the unit's last tile
-  join[blockIdx.x] =
-      PagedJoin{x.b, x.kh, x.blk, paged_owner(st.total, st.ctas, end) - (int32_t)blockIdx.x + 1};
+  if (x.whole()) return;
+  // the unit's first and last tile in the launch's list (x is the CTA's last
+  // piece where it begins the unit, its first where it does not)
+  const int64_t begin = x.begins() ? st.first + st.count - x.j1 : st.first - x.j0;
+  const PagedShares shares(st.total, st.ctas);
+  const int32_t first = shares.owner(begin);
+  join[2 * blockIdx.x + (x.begins() ? 1 : 0)] =
+      PagedJoin{x.b, x.kh, x.blk, first, shares.owner(begin + x.cost - 1) - first + 1};
 }
 
 }  // namespace varlen

@@ -276,7 +276,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             const uint32_t s = pos % C::NSLOT;
             if (!mbar_wait(&sh.kv_full[s], (pos / C::NSLOT) & 1, abort)) break;
             tc_fence_after();
-            for (int hf = 0; hf < nh; ++hf) issue_s(hf, s);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+              if (hf < nh) issue_s(hf, s);
             mma_commit(&sh.kv_empty[s]);
             if (tiles == 1) mma_commit(&sh.q_empty);
           }
@@ -287,7 +289,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             if (!E4M3 && !mbar_wait(&sh.v_ok[vs], (vpos / C::NSLOT) & 1, abort)) { ok = false; break; }
             const int nk = (min(kChunkTile, x.u.hi - (x.u.tile0 + x.j0 + j) * kChunkTile) + 15) >> 4;
             if (more && !mbar_wait(&sh.kv_full[ks], (kpos / C::NSLOT) & 1, abort)) { ok = false; break; }
-            for (int hf = 0; hf < nh; ++hf) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              if (hf >= nh) break;
               if (!mbar_wait(&sh.p_full[hf], (g[hf] + j) & 1, abort)) { ok = false; break; }
               tc_fence_after();
               issue_pv(hf, vs, j == 0, nk);
@@ -300,7 +304,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
               if (j + 2 == tiles) mma_commit(&sh.q_empty);
             }
           }
-          for (int hf = 0; hf < nh; ++hf) g[hf] += tiles;
+          g[0] += tiles;
+          if (nh == 2) g[1] += tiles;
           pos += 2 * tiles;
         }
         // Drain: every MMA this thread issued completes before TMEM is freed.

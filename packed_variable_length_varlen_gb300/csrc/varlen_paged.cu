@@ -165,19 +165,22 @@ constexpr int kRowsWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kRowsWarps * 32)
-    varlen_paged_join_rows_kernel(const PagedParams p, const PagedParts parts) {
+    varlen_paged_join_rows_kernel(const PagedParams p, const PagedParts parts, bool behind) {
   __shared__ float weight[kRowsWarps][2 * kMaxSms];
-  dependency_wait();
+  // behind the other join, which waited for both kernels: only before it ends
+  if (!behind) dependency_wait();
   const PagedJoin u = parts.join[2 * blockIdx.x + 1];
   dependents_may_launch();
-  if (u.parts == 0) return;
-  const int32_t warp = threadIdx.x >> 5, row = blockIdx.y * kRowsWarps + warp;
-  const int32_t q0 = clamp_row(__ldg(p.cu_q + u.b), p.total_q), q1 = clamp_row(__ldg(p.cu_q + u.b + 1), p.total_q);
-  const int32_t half_tokens = kChunkRows / 2 / p.group;
-  const int32_t half = row >> 7, in_half = row & 127, t = in_half / p.group;
-  const int64_t tok = (int64_t)u.blk * 2 * half_tokens + half * half_tokens + t;
-  if (t >= half_tokens || tok >= q1 - q0) return;
-  join_by_warp<D>(p, parts, u, row, JoinRow{q0 + tok, u.kh * p.group + in_half - t * p.group}, weight[warp]);
+  if (u.parts != 0) {
+    const int32_t warp = threadIdx.x >> 5, row = blockIdx.y * kRowsWarps + warp;
+    const int32_t q0 = clamp_row(__ldg(p.cu_q + u.b), p.total_q), q1 = clamp_row(__ldg(p.cu_q + u.b + 1), p.total_q);
+    const int32_t half_tokens = kChunkRows / 2 / p.group;
+    const int32_t half = row >> 7, in_half = row & 127, t = in_half / p.group;
+    const int64_t tok = (int64_t)u.blk * 2 * half_tokens + half * half_tokens + t;
+    if (t < half_tokens && tok < q1 - q0)
+      join_by_warp<D>(p, parts, u, row, JoinRow{q0 + tok, u.kh * p.group + in_half - t * p.group}, weight[warp]);
+  }
+  if (behind) dependency_wait();
 }
 
 template <int D>
@@ -187,7 +190,8 @@ cudaError_t launch_join_d(const PagedLaunch& L, cudaStream_t stream) {
     e = launch_overlapped(varlen_paged_join_kernel<D>,
                           dim3(L.sms * few_ctas(L.e4m3)), kJoinWarps * 32, 0, stream, L.p, L.few_parts);
   if (e == cudaSuccess && L.many)
-    e = launch_overlapped(varlen_paged_join_rows_kernel<D>, dim3(L.sms, kChunkRows / kRowsWarps), kRowsWarps * 32, 0, stream, L.p, L.chunk);
+    e = launch_overlapped(varlen_paged_join_rows_kernel<D>, dim3(L.sms, kChunkRows / kRowsWarps), kRowsWarps * 32, 0, stream, L.p, L.chunk,
+                          L.few);
   return e;
 }
 

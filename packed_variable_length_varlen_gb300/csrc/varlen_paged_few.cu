@@ -106,10 +106,14 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-// mbar_wait by a whole warp, its outcome the same in every lane.
+// mbar_wait by a whole warp, its outcome the same in every lane.  The loop
+// stands apart, so that the way through a tile stays short.
+__device__ __noinline__ bool warp_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+  return warp_wait_long(bar, parity, abort);
 }
 
 template <class T>
@@ -306,7 +310,14 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
         band_keys(x.u.t0, x.u.t0, x.n, x.sk, p.win_left, p.win_right, &a, &all_hi);
       }
       const int32_t tiles = min(x.j1, x.u.tiles);
-      for (int32_t j = x.j0; j < tiles; ++j, pos += 2) {
+      if (!works) {  // no rows: only gives the slots back
+        for (int32_t j = 2 * x.j0; ok && j < 2 * tiles; ++j, ++pos) {
+          const uint32_t slot = pos % C::NSLOT;
+          ok = warp_wait(&sh.full[slot], (pos / C::NSLOT) & 1, abort);
+          if (ok && lane == 0) mbar_arrive(&sh.empty[slot]);
+        }
+      }
+      for (int32_t j = works ? x.j0 : tiles; j < tiles; ++j, pos += 2) {
         const uint32_t ks = pos % C::NSLOT, vs = (pos + 1) % C::NSLOT;
         if (!warp_wait(&sh.full[ks], (pos / C::NSLOT) & 1, abort)) {
           ok = false;
@@ -324,7 +335,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
 #pragma unroll 1
         for (int a = kg * C::STEP; a < C::KT; a += share * C::STEP) {
           float s[4], s2[4];  // keys a + r and a + r + 8 of rows 2c, 2c + 1; s2: a second chain of products
-          if (works) {
+          {
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[e] = s2[e] = 0.f;
             constexpr int NL = E4M3 ? C::KSTEPS / 4 : C::KSTEPS / 2;  // 16-byte loads of a key
@@ -367,7 +378,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.empty[ks]);
           }
-          if (works) {
+          {
             if (edge) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -412,7 +423,6 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
           }
           if (!ok) break;
           __syncwarp();
-          if (!works) continue;
           uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;  // keys 2c, 2c+1 and 2c+8, 2c+9
           if (vedge) {
             auto in = [&](int k) { return key0 + a + k >= x.u.lo && key0 + a + k < x.u.hi; };

@@ -1,0 +1,156 @@
+"""More of the paged cache on a GPU: empty calls, stale codes, larger shapes
+drawn at random, calls by way of the bounds-checking build, and the raw entry
+points with a caller's workspace."""
+import math
+import os
+import random
+import subprocess
+import sys
+
+import pytest
+import torch
+
+from tests import paged_cases as C
+from tests.test_paged_gpu import _attend, _ok, _q
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def va():
+    from packed_variable_length_varlen_gb300 import varlen_attn
+    return varlen_attn
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_nothing_to_do(va, kind):
+    """No rows, no keys, no segments with rows."""
+    cache, _, _ = C.make_cache([0, 0], 2, 64, 16, kind, DEV)
+    cu = C.cu_of([0, 0], DEV)
+    none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    va.cache_write(cache, none, none, cu)
+    k, v = va.cache_read(cache, cu, 0)
+    assert k.shape == (0, 2, 64)
+    out, lse = va.attention_fwd_paged(torch.empty(0, 4, 64, dtype=torch.bfloat16, device=DEV), cache, cu)
+    assert out.shape == (0, 4, 64) and lse.shape == (4, 0)
+    for rows in (3, 90):  # rows, but in no segment
+        q = _q(rows, 4, 64)
+        out = torch.full_like(q, 9.0)
+        va.attention_fwd_paged(q, cache, cu, out=out)
+        assert (out == 9.0).all()
+        va.cache_write(cache, _q(rows, 2, 64), _q(rows, 2, 64), cu)
+    for new in ([1, 2], [80, 3]):  # segments with rows and without keys
+        out, lse = va.attention_fwd_paged(_q(sum(new), 4, 64), cache, C.cu_of(new, DEV))
+        assert (out == 0).all() and (lse == -math.inf).all()
+    _ok(va)
+
+
+@pytest.mark.parametrize("n", [1, 9, 100])
+def test_stale_codes_may_be_anything(va, n):
+    """Codes that stand for NaN, and NaN scales, behind the sequence's end and before the window."""
+    cache, k, v = C.make_cache([333], 2, 128, 64, "e4m3", DEV)
+    left = 40
+    first = 333 - n - left
+    for t in (cache.k_pages, cache.v_pages):
+        raw = t.view(torch.uint8)
+        for pg in range(raw.shape[0]):
+            pos = (cache.block_table[0] == pg).nonzero()
+            base = int(pos[0]) * 64 if len(pos) else 10 ** 6
+            for row in range(64):
+                if not first <= base + row < 333:
+                    raw[pg, row] = 0x7f if row % 2 else 0xff
+    q = _q(n, 8, 128)
+    out, lse = va.attention_fwd_paged(q, cache, C.cu_of([n], DEV), max_seqlen_q=n, causal=True, window=(left, -1))
+    _ok(va)
+    ref = C.attend(q, k[0][first:], v[0][first:], float(torch.tensor(128 ** -0.5)), left, 0)
+    C.check_attend(out, lse, ref, 128, 333)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_drawn_shapes(va, seed):
+    """Shapes drawn over the whole range that the entry points allow, small enough for the plain form."""
+    r = random.Random(seed)
+    kind = r.choice(("bf16", "e4m3"))
+    kv = r.choice((1, 2, 3, 8))
+    group = r.choice((1, 2, 3, 5, 7, 8, 12, 16, 33))
+    batch = r.choice((1, 2, 5, 40))
+    most = r.choice((1, 4, 30, 250))
+    new = [r.randint(0 if most > 1 else 1, most) for _ in range(batch)]
+    lens = [r.randint(0, r.choice((20, 300, 2500))) for _ in range(batch)]
+    _attend(va, new, lens, kv * group, kv, r.choice((64, 96, 128)), r.choice((16, 32, 64, 128, 256, 512, 1024)), kind,
+            r.random() < 0.7, (r.choice((-1, -1, 0, 5, 100, 1000)), r.choice((-1, 0, 3, 64))),
+            order=r.choice(("nhd", "hnd", "padded", "together")), hint=r.choice((0, max(new))), seed=seed,
+            pad=r.choice((0, 8)), extra=r.randint(0, 3))
+
+
+@pytest.mark.parametrize("new", [[3, 1], [200, 5], [70]])
+def test_raw_call_with_a_workspace_that_holds_anything(va, new):
+    """The C entry point with a caller's workspace of just the size, full of NaN, between canaries; the same bits
+    as a call with another one."""
+    lens = [5000, 300][:len(new)]
+    H, kv, D = 8, 2, 128
+    cache, k, v = C.make_cache(lens, kv, D, 64, "e4m3", DEV)
+    total = sum(new)
+    q, cu = _q(total, H, D), C.cu_of(new, DEV)
+    need = va.varlen_attn_fwd_paged_workspace_size(len(new), total, H, kv, D)
+    got = []
+    for fill in (0x00, 0xff, 0x7f):
+        ws = torch.full((need + 512,), fill, dtype=torch.uint8, device=DEV)
+        ws[need:] = 0xa5
+        out = torch.empty(total, H, D, dtype=torch.bfloat16, device=DEV)
+        lse = torch.empty(H, total, device=DEV)
+        st = va.varlen_attn_fwd_paged(q, cu, len(new), total, H, 0, cache.struct, D ** -0.5, -1, 0, out, lse, ws, need)
+        assert st == 0, va.varlen_attn_status_string(st)
+        _ok(va)
+        assert (ws[need:] == 0xa5).all()
+        got.append((out, lse))
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+    # a table shared by every sequence (row stride 0), as the C struct allows
+    if len(new) == 2:
+        s = va.VarlenKvCache.from_buffer_copy(cache.struct)
+        s.table_stride = 0
+        both = torch.tensor([300, 300], dtype=torch.int32, device=DEV)
+        s.seqlens = both.data_ptr()
+        st = va.varlen_attn_fwd_paged(q, cu, 2, total, H, 0, s, D ** -0.5, -1, 0, out, lse, ws, need)
+        assert st == 0
+        _ok(va)
+        ref = C.attend(q[new[0]:], k[0][:300], v[0][:300], float(torch.tensor(D ** -0.5)), -1, 0)
+        C.check_attend(out[new[0]:], lse[:, new[0]:], ref, D, 300)
+
+
+def test_a_call_on_another_stream_waits_for_its_allocations(va):
+    """What a call allocates on the current stream may still be in use there: the call on another stream comes after."""
+    cache, k, v = C.make_cache([700], 2, 64, 16, "bf16", DEV)
+    q, cu = _q(100, 4, 64), C.cu_of([100], DEV)
+    want = va.attention_fwd_paged(q, cache, cu, causal=True)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(10):
+        busy = torch.empty(100 * 4 * 64, dtype=torch.bfloat16, device=DEV)
+        for _ in range(20):
+            busy.fill_(1.0)
+        del busy  # its memory goes to the next allocation while the fills are still to run
+        out, lse = va.attention_fwd_paged(q, cache, cu, causal=True, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    handle = side.cuda_stream
+    out, lse = va.attention_fwd_paged(q, cache, cu, causal=True, stream=handle)
+    kk, vv = va.cache_read(cache, C.cu_of([700], DEV), 700, stream=handle)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(kk, k[0].to(torch.bfloat16)) and torch.equal(vv, v[0].to(torch.bfloat16))
+    _ok(va)
+
+
+def test_bounds_checked_build():
+    """The cases of the other file on the build whose kernels check every plain global access."""
+    from packed_variable_length_varlen_gb300 import build
+    lib = build.build(bounds=True)
+    env = dict(os.environ, VARLEN_ATTN_LIB=lib)
+    r = subprocess.run([sys.executable, "-m", "pytest", "tests/test_paged_gpu.py", "-q", "-x", "-m", "gpu", "-k",
+                        "write_then_read or few_rows or test_chunks or layouts or head_groups or long_cache or bad_pages",
+                        "-p", "no:cacheprovider"], cwd=ROOT, env=env, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-2000:]

@@ -97,16 +97,22 @@ struct PagedParams {
   PageView pages;
   const int32_t* cu_q;
   int32_t batch, total_q, num_heads, kv_heads, group;
+  int32_t few_rows;  // up to which the kernel for few rows takes a segment
   int64_t win_left, win_right;
   float scale_log2;
   unsigned int* err;
   Span q_span, out_span, lse_span, kp_span, vp_span, ks_span, vs_span;  // bounds-checking build
 };
 
-// What a kernel takes: segments of at most kFewRows rows, of more, or all.
+// What a kernel takes: segments of at most few_rows() rows, of more, or all.
 enum PagedTake : int32_t { kTakeFew = 0, kTakeMany = 1, kTakeAll = 2 };
 
-constexpr int kFewRows = 32;      // rows (queries x heads of a group) of a unit of the kernel for few rows
+// Rows (queries x heads of a group) up to which the kernel for few rows takes a
+// segment, and rows of its units.  64 sequences of up to 8192 keys, 8 key heads
+// of 128, us for the kernel for few rows and the one for many: bf16 16 rows 174
+// and 212, 32 rows 250 and 212; E4M3 16 rows 170 and 269, 32 rows 287 and 270.
+constexpr int few_rows(bool e4m3) { return e4m3 ? 32 : 16; }
+constexpr int kMostFewRows = 32;
 constexpr int kFewTile = 64;      // keys per tile of that kernel
 // its CTAs on an SM: E4M3 rows are half as long, so more of them have to be in the making
 constexpr int few_ctas(bool e4m3) { return e4m3 ? 3 : 2; }
@@ -143,12 +149,12 @@ struct PagedLaunch {
 };
 
 // Byte offsets of the workspace.  (A call whose rows all together are no more
-// than kFewRows has no segment for the kernel for many rows.)
+// than few_rows() has no segment for the kernel for many rows.)
 struct PagedWorkspace {
   size_t few_o, few_ml, few_join, chunk_o, chunk_ml, chunk_join, bytes;
   int32_t few_rows;
 };
-inline PagedWorkspace paged_workspace(int64_t total_rows, int32_t head_dim) {
+inline PagedWorkspace paged_workspace(int64_t total_rows, int32_t head_dim) {  // of either type
   size_t at = 0;
   auto take = [&at](size_t bytes) {
     const size_t a = at;
@@ -156,8 +162,8 @@ inline PagedWorkspace paged_workspace(int64_t total_rows, int32_t head_dim) {
     return a;
   };
   PagedWorkspace w;
-  w.few_rows = (int32_t)(total_rows < kFewRows ? (total_rows < 1 ? 1 : total_rows) : kFewRows);
-  const size_t few = (size_t)few_ctas(true) * kMaxSms, many = total_rows > kFewRows ? kMaxSms : 0;
+  w.few_rows = (int32_t)(total_rows < kMostFewRows ? (total_rows < 1 ? 1 : total_rows) : kMostFewRows);
+  const size_t few = (size_t)few_ctas(true) * kMaxSms, many = total_rows > few_rows(false) ? kMaxSms : 0;
   w.few_o = take(2 * few * w.few_rows * head_dim * 4);
   w.few_ml = take(2 * few * w.few_rows * 8);
   w.few_join = take(2 * few * sizeof(PagedJoin));

@@ -235,6 +235,7 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   p.num_heads = num_heads;
   p.kv_heads = c.num_kv_heads;
   p.group = num_heads / c.num_kv_heads;
+  p.few_rows = few_rows(c.type == VARLEN_CACHE_E4M3);
   p.win_left = window_left < 0 ? kWinUnbounded : window_left;
   p.win_right = window_right < 0 ? kWinUnbounded : window_right;
   p.scale_log2 = scale * kLog2e;
@@ -253,8 +254,8 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   // alone; a single segment of more rows goes to the other one whatever its
   // length; otherwise both run and each takes the segments that are its own.
   const int64_t total_rows = (int64_t)total_q * p.group;
-  L.few = total_rows <= kFewRows || batch > 1 || (max_seqlen_q > 0 && (int64_t)max_seqlen_q * p.group <= kFewRows);
-  L.many = total_rows > kFewRows && !(max_seqlen_q > 0 && (int64_t)max_seqlen_q * p.group <= kFewRows);
+  L.few = total_rows <= p.few_rows || batch > 1 || (max_seqlen_q > 0 && (int64_t)max_seqlen_q * p.group <= p.few_rows);
+  L.many = total_rows > p.few_rows && !(max_seqlen_q > 0 && (int64_t)max_seqlen_q * p.group <= p.few_rows);
   char* ws = static_cast<char*>(workspace);
   const PagedWorkspace w = paged_workspace(total_rows, c.head_dim);
   L.few_parts = PagedParts{reinterpret_cast<float*>(ws + w.few_o), reinterpret_cast<float*>(ws + w.few_ml),

@@ -58,7 +58,8 @@ struct FewCfg {
   static constexpr int THREADS = (WARPS + 1) * 32;
   static constexpr int KT = kFewTile;                       // keys per tile
   static constexpr int STEP = 16;                           // keys a warp takes at a time
-  using Geom = PagedGeom<kFewRows, KT, false>;
+  static constexpr int ROWS = few_rows(E4M3);
+  using Geom = PagedGeom<ROWS, KT, false>;
   static constexpr int CK = E4M3 ? 1 : (D + 63) / 64;       // 128-byte column chunks of a row
   static constexpr int CHUNK = KT * 128;
   static constexpr int TILE = CK * CHUNK;
@@ -247,8 +248,8 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
     walk.init(sh.start, p, take);
     while (ok && walk.next(p, x)) {
       // rows of the unit: first is row `skip` of token t0
-      const int32_t skip = x.blk * kFewRows - x.u.t0 * p.group;
-      const int32_t rows = min((x.n - x.u.t0) * p.group - skip, kFewRows);
+      const int32_t skip = x.blk * C::ROWS - x.u.t0 * p.group;
+      const int32_t rows = min((x.n - x.u.t0) * p.group - skip, C::ROWS);
       const int mt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);  // row tiles
       const int rt = warp & (mt - 1), kg = warp / mt, share = C::WARPS / mt;
       const bool works = rt * 8 < rows;

@@ -87,7 +87,6 @@ struct PieceReader {
   }
 };
 
-__device__ __forceinline__ uint32_t raw_pair(uint32_t x) { return (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u); }
 __device__ __forceinline__ uint32_t mul_pair(uint32_t a, uint32_t b) {
   const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&x);
@@ -361,7 +360,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
       const int32_t tiles = min(x.j1, x.u.tiles) - x.j0;
       if (hf == 1 && x.u.t1 - x.u.t0 < half_tokens) continue;  // no rows in this half
       float m_use = -INFINITY, l = 0.f;
-      int32_t key_lo = 0, key_hi = 0;
+      // a row that is none sees all keys: what it computes goes nowhere, and its
+      // warp is spared the selects
+      int32_t key_lo = 0, key_hi = INT32_MAX;
       if (live) band_keys(tok, tok, x.n, x.sk, p.win_left, p.win_right, &key_lo, &key_hi);
       const int32_t key0 = (x.u.tile0 + x.j0) * kChunkTile;
       for (int32_t j = 0; j < tiles; ++j) {
@@ -541,8 +542,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
               uint32_t y[8];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                y[2 * e] = mul_pair(raw_pair(__byte_perm(w[e], 0, 0x1000)), ff);
-                y[2 * e + 1] = mul_pair(raw_pair(__byte_perm(w[e], 0, 0x3020)), ff);
+                // the upper and the lower bytes of four bf16, then two and two of them
+                const uint32_t h = (w[e] & 0x80808080u) | ((w[e] >> 4) & 0x07070707u), l = (w[e] * 16u) & 0xf0f0f0f0u;
+                y[2 * e] = mul_pair(__byte_perm(l, h, 0x5140), ff);
+                y[2 * e + 1] = mul_pair(__byte_perm(l, h, 0x7362), ff);
               }
               *reinterpret_cast<uint4*>(to + (((2 * k) ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
               *reinterpret_cast<uint4*>(to + (((2 * k + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);

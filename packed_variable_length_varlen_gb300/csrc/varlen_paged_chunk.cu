@@ -53,9 +53,9 @@ struct ChunkCfg {
   static constexpr int KSTEPS = D / 16;
   static constexpr int SMEM = 1024 + TILE * (2 + NSLOT) + NRAW * (CHUNK + SCALES);
   // Registers (threads x registers at launch is all there is to share out):
-  // bf16 384 x 168 = 128 x (120 + 192 + 192); E4M3 512 x 128 = 128 x (72 + 184 + 184 + 72).
-  static constexpr uint32_t REGS_LAUNCH = E4M3 ? 128 : 168, REGS_CTL = E4M3 ? 72 : 120, REGS_SOFTMAX = E4M3 ? 184 : 192,
-                            REGS_CONVERT = 72;
+  // bf16 384 x 168 = 128 x (120 + 192 + 192); E4M3 512 x 128 = 128 x (80 + 184 + 184 + 64).
+  static constexpr uint32_t REGS_LAUNCH = E4M3 ? 128 : 168, REGS_CTL = E4M3 ? 80 : 120, REGS_SOFTMAX = E4M3 ? 184 : 192,
+                            REGS_CONVERT = 64;
   static_assert(REGS_CTL + 2 * REGS_SOFTMAX + (E4M3 ? REGS_CONVERT : 0) <= (THREADS / 128) * REGS_LAUNCH,
                 "warpgroup register split exceeds the launch allocation");
 };

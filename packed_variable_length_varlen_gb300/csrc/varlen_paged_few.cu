@@ -387,15 +387,16 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
                 s[e] = key >= klo[e & 1] && key < khi[e & 1] ? s[e] : -INFINITY;
               }
             }
+            // The maximum follows only when a key passes it by more than 2^8 (o and l
+            // carry the same factor, so nothing is lost): the lanes of a row need to
+            // look at one another's keys only then.
             float mx[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
-#pragma unroll
-            for (int w = 4; w < 32; w <<= 1) {
-              mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], w));
-              mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], w));
-            }
-            // the maximum follows only when it grew by more than 2^8: o and l
-            // carry the same factor, so nothing is lost
             if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+#pragma unroll
+              for (int w = 4; w < 32; w <<= 1) {
+                mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], w));
+                mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], w));
+              }
               float al[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {

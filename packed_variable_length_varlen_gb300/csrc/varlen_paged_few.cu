@@ -64,7 +64,7 @@ struct FewCfg {
   static constexpr int CHUNK = KT * 128;
   static constexpr int TILE = CK * CHUNK;
   static constexpr int SCALES = E4M3 ? KT * 8 : 0;          // page pieces of at least 16 keys, 128 bytes apart
-  static constexpr int NSLOT = E4M3 ? 7 : (CK == 1 ? 8 : 5);
+  static constexpr int NSLOT = E4M3 ? 4 : (CK == 1 ? 6 : 4);
   static constexpr int KSTEPS = E4M3 ? (D == 64 ? 4 : 8) : CK * 4;
   static constexpr int MT = D / 16;                         // m-tiles of O^T
   static constexpr int XCHG = (MT * 4 + 4) * 32 * 4;        // one warp's (o, m, l)

@@ -123,7 +123,8 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
 
 // 3-D tiled load of one box into shared memory; completion is signalled on
 // `bar` as transaction bytes.  Coordinates are element indices {x, y, z};
-// x * 2 bytes is a multiple of 16 for every call site (x in {0, 64}).
+// x * 2 bytes is a multiple of 16 for every call site (x in {0, 64}, or the
+// first of a page piece's scales, a multiple of 16).
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
                                             int32_t x, int32_t y, int32_t z) {
   asm volatile(

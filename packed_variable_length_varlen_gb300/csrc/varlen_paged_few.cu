@@ -1,9 +1,9 @@
 // varlen_paged_few.cu -- attention over the paged cache for few query rows:
 // single tokens, drafted tokens, short chunks.
 //
-// Bound: every key and value is read once for at most 32 rows (query tokens
-// times the query heads that share a key head), so the memory's rate decides
-// and the matrix products only have to keep up with it.  At 6.8 TB/s an SM
+// Bound: every key and value is read once for at most 16 (bf16) or 32 (E4M3)
+// rows (query tokens times the query heads that share a key head), so the
+// memory's rate decides and the matrix products only have to keep up with it.  At 6.8 TB/s an SM
 // receives 44.7 bytes a nanosecond, 12 bf16 or 23 E4M3 elements a cycle.  The
 // warp-level m16n8k16 products take keys (then columns of V) as their 16 rows
 // and query rows as their 8 columns, S^T = K Q^T and O^T = V^T P^T: a step of 16
@@ -11,9 +11,16 @@
 // enough warps stay resident to hide the chain of products, softmax and
 // products.  (The other way round, 16 query rows by 8 keys, costs twice the
 // products and registers while most of the 16 rows are empty: 214 us where this
-// form takes FIGURE for 64 ragged E4M3 sequences.)
+// form took 190 for 64 ragged E4M3 sequences, and 124 with the third CTA an SM that
+// its registers leave room for.)  Measured: 8 sequences of 17580 bf16 keys, 56
+// heads of 128, one token: 565-584 us across machines, 6.9-7.1 TB/s, the copy
+// rate.  64 E4M3 sequences of 1..8192 keys, 8 key heads: 112-118 us, 4.4-4.6 TB/s;
+// TMA delivers a row of at most 128 bytes every 5 to 6 cycles, so that half as
+// long rows come at a lower rate, and a call's fixed parts (its start, 4 us until
+// the first tile, and the join, 5 us) weigh more.
 //
-// A CTA is a few consumer warps and a producer warp; two CTAs share an SM.
+// A CTA is four consumer warps and a producer warp; two (bf16) or three (E4M3)
+// CTAs share an SM.
 // The producer streams tiles of K and of V, page piece by page piece, through
 // a ring of shared-memory slots by TMA (an entry that names no page, and
 // positions past the sequence, become an out-of-range page: zeros, no
@@ -64,6 +71,9 @@ struct FewCfg {
   static constexpr int CHUNK = KT * 128;
   static constexpr int TILE = CK * CHUNK;
   static constexpr int SCALES = E4M3 ? KT * 8 : 0;          // page pieces of at least 16 keys, 128 bytes apart
+  // Slots of K or V tiles: four are enough to cover the memory's latency, and
+  // more are slower (64 E4M3 sequences 116 us with four, 118 with five, 125 with
+  // seven; 56 bf16 heads 584 with four, 592 with five).
   static constexpr int NSLOT = E4M3 ? 4 : (CK == 1 ? 6 : 4);
   static constexpr int KSTEPS = E4M3 ? (D == 64 ? 4 : 8) : CK * 4;
   static constexpr int MT = D / 16;                         // m-tiles of O^T

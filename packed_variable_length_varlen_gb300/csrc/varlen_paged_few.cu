@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
             rowf[i] *= __uint_as_float((uint32_t)(__shfl_sync(0xffffffffu, e, (2 * c + i) * 4) - 14) << 23);
         }
       }
-      float vref = 0.f, vinv = 0.f;  // E4M3: R and 2^7 / R
+      float vref = 0.f, vinv = 0.f;  // E4M3: R and 1 / R (finite: R >= 2^-127)
       float o[C::MT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
       for (int t = 0; t < C::MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
               if (top > vref) {
                 const float f = vref / top;  // powers of two (or 0)
                 vref = top;
-                vinv = 0x1p7f / top;
+                vinv = 1.f / top;
 #pragma unroll
                 for (int t = 0; t < C::MT; ++t)
 #pragma unroll
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
               }
             }
             if (!wide) {
-              const float f0 = sv[0] * vinv, f1 = sv[1] * vinv;
+              const float f0 = sv[0] * vinv * 0x1p7f, f1 = sv[1] * vinv * 0x1p7f;
               const uint32_t p0 = transpose8(pack_f16x2(s[0] * f0, s[1] * f0));
               const uint32_t p1 = transpose8(pack_f16x2(s[2] * f1, s[3] * f1));
 #pragma unroll
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
                 mma16816<true>(o[t], a0, a1, a2, a3, p0, p1);
               }
             } else {
-              const float up = vref > 0.f ? 1.f / vref : 1.f;
+              const float up = vref > 0.f ? vinv : 1.f;
               // the factors of keys 2c, 2c + 1 and 2c + 8, 2c + 9
               uint32_t f[2];
 #pragma unroll

@@ -122,6 +122,55 @@ def test_raw_call_with_a_workspace_that_holds_anything(va, new):
         C.check_attend(out[new[0]:], lse[:, new[0]:], ref, D, 300)
 
 
+@pytest.mark.parametrize("n", [1, 9, 100])
+@pytest.mark.parametrize("shift", [-121, -119, -60, 60, 118])
+def test_value_scales_at_the_ends_of_their_range(va, n, shift):
+    """Values near the least and the largest scale (2^-127 and beyond): the output is that of ordinary values times
+    the same power of two, bit for bit where both are quantised alike, else within the roundings."""
+    ln, dim, heads = 200, 64, 2
+    k, v = _q(ln, heads, dim, 5), _q(ln, heads, dim, 6)
+    q, cu = _q(n, 4, dim, 7), C.cu_of([n], DEV)
+    got = []
+    for e in (0, shift):
+        cache, _, _ = C.make_cache([ln], heads, dim, 16, "e4m3", DEV)
+        va.cache_write(cache, k, (v.double() * 2.0 ** e).to(torch.bfloat16), C.cu_of([ln], DEV))
+        out, lse = va.attention_fwd_paged(q, cache, cu, max_seqlen_q=n, causal=True)
+        _ok(va)
+        kk, vv = va.cache_read(cache, C.cu_of([ln], DEV), ln)
+        # held values from the codes: reading back rounds where bf16 is subnormal
+        pos = torch.arange(ln, device=DEV)
+        pg = cache.block_table[0].long()[pos // 16]
+        held = cache.v_pages.view(torch.uint8)[pg, pos % 16].view(torch.float8_e4m3fn).double() * \
+            cache.v_scale[pg, :, pos % 16].double()[..., None]
+        o, _, A, S = C.attend(q, kk.double(), held, 0.125, -1, 0)
+        assert torch.isfinite(out).all()
+        # P to bf16 or f16, the score's sum and exp2, O to bf16 (2^-134: half of bf16's least step)
+        tol = 2.0 ** -8 * (A + o.abs()) + 2.0 ** -14 * A + 2.0 ** -134
+        d = (out.double() - o).abs()
+        assert (d <= tol).all(), (e, float((d / tol).max()))
+        got.append((out.double() * 2.0 ** -e, lse))
+    assert torch.equal(got[0][1], got[1][1])
+    if shift > -119:
+        assert torch.equal(got[0][0], got[1][0])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 9, 100])
+@pytest.mark.parametrize("shift", [-80, 80])
+def test_queries_and_keys_of_opposite_sizes(va, kind, n, shift):
+    """Queries times 2^shift and keys times 2^-shift: the same scores, the same bits."""
+    ln, dim, heads = 200, 128, 2
+    k, v = _q(ln, heads, dim, 5), _q(ln, heads, dim, 6)
+    q, cu = _q(n, 4, dim, 7), C.cu_of([n], DEV)
+    got = []
+    for e in (0, shift):
+        cache, _, _ = C.make_cache([ln], heads, dim, 32, kind, DEV)
+        va.cache_write(cache, (k.double() * 2.0 ** -e).to(torch.bfloat16), v, C.cu_of([ln], DEV))
+        got.append(va.attention_fwd_paged((q.double() * 2.0 ** e).to(torch.bfloat16), cache, cu, max_seqlen_q=n, causal=True))
+        _ok(va)
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 def test_a_call_on_another_stream_waits_for_its_allocations(va):
     """What a call allocates on the current stream may still be in use there: the call on another stream comes after."""
     cache, k, v = C.make_cache([700], 2, 64, 16, "bf16", DEV)

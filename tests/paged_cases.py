@@ -28,7 +28,7 @@ def quantise(x):
     return torch.clamp(y, -E4M3_MAX, E4M3_MAX).float().to(torch.float8_e4m3fn), s.to(torch.bfloat16)
 
 
-def make_cache(lens, heads, dim, page, kind, device, seed=0, order="nhd", spare=3, amp=1.0, fill=None):
+def make_cache(lens, heads, dim, page, kind, device, seed=0, order="nhd", spare=3, amp=1.0, fill=None, columns=1):
     """A PagedCache of random pages in random order with lens[b] positions each; pages no sequence uses and rows
     past a sequence's end hold NaN (bf16) or NaN scales.  Returns (cache, k, v): lists of [lens[b], heads, dim]
     float64 held values."""
@@ -36,7 +36,7 @@ def make_cache(lens, heads, dim, page, kind, device, seed=0, order="nhd", spare=
     g = torch.Generator().manual_seed(seed)
     need = [-(-n // page) for n in lens]
     pages = sum(need) + spare
-    width = max(need + [1])
+    width = max(need + [columns])
     perm = torch.randperm(pages, generator=g).tolist()
     table = torch.full((len(lens), width), -7, dtype=torch.int32)
     at = 0

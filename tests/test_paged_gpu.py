@@ -36,9 +36,10 @@ def _q(total, heads, dim, seed=1, amp=1.0, pad=0):
 
 
 def _attend(va, new, lens, heads, kv, dim, page, kind, causal=False, window=(-1, -1), order="nhd", hint=None, seed=0,
-            amp=1.0, extra=0, pad=0, fill=None):
+            amp=1.0, extra=0, pad=0, fill=None, columns=1):
     """Runs the attention, checks it; returns (out, lse)."""
-    cache, k, v = C.make_cache(lens, kv, dim, page, kind, DEV, seed=seed, order=order, amp=amp, fill=fill)
+    cache, k, v = C.make_cache(lens, kv, dim, page, kind, DEV, seed=seed, order=order, amp=amp, fill=fill,
+                               columns=columns)
     total = sum(new) + extra
     q = _q(total, heads, dim, seed=seed + 1, amp=amp, pad=pad)
     cu = C.cu_of(new, DEV)

@@ -86,6 +86,18 @@ def test_drawn_shapes(va, seed):
             pad=r.choice((0, 8)), extra=r.randint(0, 3))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("heads,kv", [(2, 2), (8, 2), (21, 3)])
+def test_both_kernels_in_one_call(va, kind, dim, heads, kv):
+    """Tables wide enough for long sequences: each segment goes to the kernel that its own length calls for, and a
+    unit that several CTAs share is joined for both."""
+    wide = 64 * 160 * 128 // 1024  # columns of 1024 positions that two segments' tables need to be taken for long
+    _attend(va, [130, 1, 0, 257, 5, 65, 33, 3, 1, 16], [700, 300, 40, 257, 128, 1000, 20, 0, 9000, 5], heads, kv, dim,
+            1024, kind, True, columns=wide, extra=2)
+    _attend(va, [1, 2, 300], [4000, 2500, 9000], heads, kv, dim, 1024, kind, True, (700, -1), columns=wide, pad=8)
+
+
 @pytest.mark.parametrize("new", [[3, 1], [200, 5], [70]])
 def test_raw_call_with_a_workspace_that_holds_anything(va, new):
     """The C entry point with a caller's workspace of just the size, full of NaN, between canaries; the same bits
@@ -203,3 +215,36 @@ def test_bounds_checked_build():
                         "write_then_read or few_rows or test_chunks or layouts or head_groups or long_cache or bad_pages",
                         "-p", "no:cacheprovider"], cwd=ROOT, env=env, capture_output=True, text=True, timeout=900)
     assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-2000:]
+
+
+def test_both_kernels_captured_and_repeated(va):
+    """A call of four launches that overlap, captured with the write before it and replayed; and two of them at once."""
+    new, lens = [1, 200, 3, 1], [5000, 900, 64, 2000]
+    cache, _, _ = C.make_cache(lens, 2, 128, 64, "e4m3", DEV, columns=64 * 160 * 128 // 64 // 4)
+    cu, total = C.cu_of(new, DEV), sum(new)
+    k, v, q = _q(total, 2, 128, 1), _q(total, 2, 128, 2), _q(total, 8, 128, 3)
+
+    def step():
+        va.cache_write(cache, k, v, cu)
+        return va.attention_fwd_paged(q, cache, cu, causal=True)
+
+    want = step()
+    torch.cuda.synchronize()
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+        got = [step() for _ in range(3)]
+    for _ in range(5):
+        for o, l in got:
+            o.zero_()
+            l.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for o, l in got:
+            assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(10):
+        res = [va.attention_fwd_paged(q, cache, cu, causal=True, stream=s) for s in streams]
+        torch.cuda.synchronize()
+        for o, l in res:
+            assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+    _ok(va)

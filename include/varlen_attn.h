@@ -340,10 +340,10 @@ int varlen_attn_fwd_fp8_dense(const void* q, varlen_dense_stride sq, const void*
  * multiples of 16 bytes below 2^40 bytes, and the (page, row, head) vectors
  * must not overlap (ordering the dimensions of extent > 1 by stride, the
  * smallest is at least head_dim and each further one at least the previous
- * extent times the previous stride; VARLEN_ERR_STRIDE).  page_size is a power
- * of two from 16 to 1024, num_pages >= 1, max_pages * page_size <= 2^31 - 2048.
- * The
- * struct itself is host memory, read during the call only.
+ * extent times the previous stride; VARLEN_ERR_STRIDE); K's vectors and V's are
+ * different ones in a cache that is written.  page_size is a power
+ * of two from 16 to 1024, num_pages >= 1, max_pages * page_size <= 2^31 - 2048,
+ * batch <= 2^30.  The struct itself is host memory, read during the call only.
  */
 enum { VARLEN_CACHE_BF16 = 0, VARLEN_CACHE_E4M3 = 1 };
 
@@ -396,8 +396,8 @@ int varlen_attn_cache_read(const varlen_kv_cache* cache, const int32_t* cu_seqle
  * Forward over the cache: packed queries q [total_q, num_heads, head_dim]
  * (bf16, cu_seqlens_q) against all seqlens[b] positions of their sequence.
  * num_heads is a multiple of the cache's num_kv_heads and at most 128 times
- * it, total_q * num_heads below 2^31 - 256 (VARLEN_ERR_SHAPE); query head h reads key head
- * h / (num_heads / num_kv_heads).  The band, out and lse are those of
+ * it, total_q * num_heads below 2^31 - 256 (VARLEN_ERR_SHAPE); query head h
+ * reads key head h / (num_heads / num_kv_heads).  The band, out and lse are those of
  * varlen_attn_fwd_window with Sk = seqlens[b]: (-1, -1) no mask, (-1, 0)
  * causal with the last query at the last key, so after
  * varlen_attn_cache_write of the same rows each sees itself and what came

@@ -13,6 +13,7 @@ using namespace varlen;
 
 namespace {
 
+constexpr int32_t kMaxBatch = 1 << 30;  // strides over the batch stay in int32
 constexpr float kLog2e = 1.4426950408889634f;
 
 int elem_bytes(const varlen_kv_cache& c) { return c.type == VARLEN_CACHE_BF16 ? 2 : 1; }
@@ -48,7 +49,7 @@ int check_pages(const varlen_kv_cache& c, varlen_page_stride s) {
 int check_cache(const varlen_kv_cache* cache, int32_t batch, int* page_shift) {
   if (cache == nullptr) return VARLEN_ERR_NULL;
   const varlen_kv_cache& c = *cache;
-  if (batch < 1 || c.num_pages < 1 || c.max_pages < 0 || c.num_kv_heads < 1 || c.table_stride < 0) return VARLEN_ERR_SHAPE;
+  if (batch < 1 || batch > kMaxBatch || c.num_pages < 1 || c.max_pages < 0 || c.num_kv_heads < 1 || c.table_stride < 0) return VARLEN_ERR_SHAPE;
   if (c.type != VARLEN_CACHE_BF16 && c.type != VARLEN_CACHE_E4M3) return VARLEN_ERR_SHAPE;
   int shift = 4;
   while (shift < 11 && (1 << shift) != c.page_size) ++shift;

@@ -6,9 +6,9 @@
 // group, head r % group.  A unit works through the key tiles that some of its
 // rows see.  The units of a launch in a fixed order (segment, key head, row
 // block), each with its tiles (at least one, so that a unit without keys is
-// visited and writes its zeros), form one long list of tiles, and CTA c of N
-// takes the tiles [c T / N, (c + 1) T / N): every CTA has the same number of
-// tiles, whatever the lengths.  A CTA's part starts and ends inside a unit
+// visited and writes its zeros), form one long list of T tiles, and each of N
+// CTAs takes T / N neighbouring ones of it (the first T % N one more): every CTA
+// has the same number of tiles, whatever the lengths.  A CTA's part starts and ends inside a unit
 // in general; what it has of a unit that it does not hold whole goes to the
 // workspace as a partial result (its running maximum, sum and unnormalised
 // output), in one of two slots: 1 for the unit that it begins and a later CTA
@@ -40,7 +40,6 @@ struct PagedUnit {
 // per tile.
 template <int ROWS, int TILE, bool BY_TOKEN>
 struct PagedGeom {
-  static constexpr int kRows = ROWS, kTile = TILE;
   __device__ static __forceinline__ int32_t half_tokens(const PagedParams& p) { return ROWS / 2 / p.group; }
   __device__ static __forceinline__ int32_t blocks(const PagedParams& p, int32_t n) {
     const uint32_t rows = BY_TOKEN ? n : n * p.group, per = BY_TOKEN ? 2 * half_tokens(p) : ROWS;
@@ -86,7 +85,6 @@ struct PagedPiece {
   int32_t b, kh, blk;
   int32_t q0, n, sk;
   int32_t j0, j1, cost;
-  int64_t after;  // tiles of the CTA's part that follow this piece
   __device__ __forceinline__ bool begins() const { return j0 == 0; }
   __device__ __forceinline__ bool ends() const { return j1 == cost; }
   __device__ __forceinline__ bool whole() const { return begins() && ends(); }
@@ -254,7 +252,6 @@ struct PagedWalk {
     x.j0 = j;
     x.j1 = (int32_t)min((int64_t)x.cost, j + left);
     left -= x.j1 - x.j0;
-    x.after = left;
     if (x.j1 == x.cost) {
       ++blk;
       j = 0;

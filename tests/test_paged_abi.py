@@ -102,6 +102,7 @@ def test_head_major_and_single_extents_are_accepted(va):
 def test_call_refusals(va):
     c = _cache(va)
     assert set(_calls(va, c, batch=0)) == {va.VARLEN_ERR_SHAPE}
+    assert set(_calls(va, c, batch=(1 << 30) + 1)) == {va.VARLEN_ERR_SHAPE}
     assert set(_calls(va, c, total=-1)) == {va.VARLEN_ERR_SHAPE}
     assert set(_calls(va, c, cu=None)) == {va.VARLEN_ERR_NULL}
     assert set(_calls(va, c, k=None)) == {va.VARLEN_ERR_NULL}
@@ -125,6 +126,7 @@ def test_attention_refusals(va):
     assert call() in (va.VARLEN_ERR_CUDA, va.VARLEN_ERR_ARCH)
     for heads in (0, -2, 3, 258):
         assert call(heads=heads, sq=(20000, 64), so=(20000, 64)) == va.VARLEN_ERR_SHAPE
+    assert call(total=2 ** 29) == va.VARLEN_ERR_SHAPE  # 2^31 rows of four heads
     for scale in (0.0, -1.0, float("inf"), float("nan")):
         assert call(scale=scale) == va.VARLEN_ERR_SHAPE
     assert call(lse=None) == va.VARLEN_ERR_NULL

@@ -198,6 +198,10 @@ def test_a_call_on_another_stream_waits_for_its_allocations(va):
         out, lse = va.attention_fwd_paged(q, cache, cu, causal=True, stream=side)
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    with torch.cuda.stream(side):  # and the other way round, on the default stream
+        out, lse = va.attention_fwd_paged(q, cache, cu, causal=True, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     handle = side.cuda_stream
     out, lse = va.attention_fwd_paged(q, cache, cu, causal=True, stream=handle)
     kk, vv = va.cache_read(cache, C.cu_of([700], DEV), 700, stream=handle)

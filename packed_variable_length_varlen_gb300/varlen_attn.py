@@ -659,6 +659,13 @@ def _packed(cache, t, heads, rows=None):
     return t.data_ptr(), VarlenStride(st[0], st[1])
 
 
+def _fresh_packed(cache, rows, heads):
+    """(tensor, pointer, strides) of new contiguous packed rows."""
+    d = cache.head_dim
+    t = torch.empty((rows, heads, d), dtype=torch.bfloat16, device=cache.device)
+    return t, t.data_ptr(), VarlenStride(heads * d, d)
+
+
 def _cu(cache, cu):
     if cu.dtype != torch.int32 or cu.dim() != 1 or cu.shape[0] != cache.batch + 1 or not cu.is_contiguous():
         raise ValueError("cu_seqlens must be contiguous int32 [batch + 1]")
@@ -708,13 +715,15 @@ def cache_read(cache, cu_seqlens, total, k=None, v=None, stream=None):
     ([total, num_kv_heads, D], allocated when None); returns (k, v)."""
     fresh = []
     if k is None:
-        k = torch.empty((total, cache.num_kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device)
+        k, kp, ks = _fresh_packed(cache, total, cache.num_kv_heads)
         fresh.append(k)
+    else:
+        kp, ks = _packed(cache, k, cache.num_kv_heads, total)
     if v is None:
-        v = torch.empty((total, cache.num_kv_heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device)
+        v, vp, vs = _fresh_packed(cache, total, cache.num_kv_heads)
         fresh.append(v)
-    kp, ks = _packed(cache, k, cache.num_kv_heads, total)
-    vp, vs = _packed(cache, v, cache.num_kv_heads, total)
+    else:
+        vp, vs = _packed(cache, v, cache.num_kv_heads, total)
     _paged_call(LIB.varlen_attn_cache_read, cache, stream, fresh,
                 (cache.ref, _cu(cache, cu_seqlens), cache.batch, total, kp, ks, vp, vs))
     return k, v
@@ -736,18 +745,19 @@ def attention_fwd_paged(q, cache, cu_seqlens_q, max_seqlen_q=0, scale=None, out=
     cu = _cu(cache, cu_seqlens_q)
     fresh = []
     if out is None:
-        out = torch.empty((total_q, H, D), dtype=torch.bfloat16, device=q.device)
+        out, op, os_ = _fresh_packed(cache, total_q, H)
         fresh.append(out)
-    op, os_ = _packed(cache, out, H, total_q)
+    else:
+        op, os_ = _packed(cache, out, H, total_q)
     if lse is None:
-        lse = torch.empty((H, total_q), dtype=torch.float32, device=q.device)
+        lse = torch.empty((H, total_q), dtype=torch.float32, device=cache.device)
         fresh.append(lse)
     elif lse.dtype != torch.float32 or tuple(lse.shape) != (H, total_q) or not lse.is_contiguous() \
             or lse.device != cache.device:
         raise ValueError("lse must be contiguous float32 [H, rows] on the cache's device")
     if workspace is None:
         nbytes = _paged_workspace_bytes(cache.batch, total_q, H, cache.num_kv_heads, D)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
         fresh.append(workspace)
     else:
         if workspace.device != cache.device:

@@ -172,7 +172,9 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
     varlen_paged_join_rows_kernel(const PagedParams p, const PagedParts parts, bool behind) {
   __shared__ float weight[kRowsWarps][2 * kMaxSms];
   // behind the other join, which waited for both kernels: only before it ends
-  if (!behind) dependency_wait();
+  // (the fence drops what this SM's L1 held before)
+  if (behind) __threadfence();
+  else dependency_wait();
   const PagedJoin u = parts.join[2 * blockIdx.x + 1];
   dependents_may_launch();
   if (u.parts != 0) {

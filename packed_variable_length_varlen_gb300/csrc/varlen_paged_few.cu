@@ -193,8 +193,10 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
   }
   // Nothing above reads or writes global memory.  Behind the kernel for many
   // rows of the same call, which waited for what came before it, this one waits
-  // only before it ends: the two share nothing but their inputs.
-  if (!behind) dependency_wait();
+  // only before it ends: the two share nothing but their inputs.  What those
+  // kernels wrote is in L2 by then; the fence drops what this SM's L1 held before.
+  if (behind) __threadfence();
+  else dependency_wait();
   paged_start<typename C::Geom>(sh.start, p, take, kLeastTiles);
   dependents_may_launch();
   PagedWalk<typename C::Geom> walk;

@@ -252,3 +252,56 @@ def test_both_kernels_captured_and_repeated(va):
         for o, l in res:
             assert torch.equal(o, want[0]) and torch.equal(l, want[1])
     _ok(va)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_both_kernels_follow_the_lengths(va, kind):
+    """Lengths, rows and a page's place that change between the replays of a captured step of four launches."""
+    new, lens = [1, 150, 2, 1], [3000, 2900, 900, 2000]
+    cache, _, _ = C.make_cache(lens, 2, 64, 64, kind, DEV, columns=64 * 160 * 128 // 64 // 4, spare=8)
+    cu, total = C.cu_of(new, DEV), sum(new)
+    start = torch.tensor([200, 700, 60, 1500], dtype=torch.int32, device=DEV)
+    grow = torch.tensor(new, dtype=torch.int32, device=DEV)
+    k, v, q = _q(total, 2, 64, 1), _q(total, 2, 64, 2), _q(total, 4, 64, 3)
+    first = cache.block_table.clone()
+    pools = [t.clone() for t in (cache.k_pages.view(torch.uint8), cache.v_pages.view(torch.uint8))]
+    scales = [None if t is None else t.clone() for t in (cache.k_scale, cache.v_scale)]
+
+    def reset():
+        cache.seqlens.copy_(start)
+        cache.block_table.copy_(first)
+        for t, old in zip((cache.k_pages, cache.v_pages), pools):
+            t.view(torch.uint8).copy_(old)
+        for t, old in zip((cache.k_scale, cache.v_scale), scales):
+            if t is not None:
+                t.copy_(old)
+
+    def step():
+        cache.seqlens.add_(grow)
+        va.cache_write(cache, k, v, cu)
+        return va.attention_fwd_paged(q, cache, cu, causal=True)
+
+    def between(i):
+        k.copy_(_q(total, 2, 64, 20 + i))
+        if i == 2:  # the first sequence's first page and the last one's change places
+            a, b = first[0, 0].clone(), first[3, 1].clone()
+            cache.block_table[0, 0], cache.block_table[3, 1] = b, a
+
+    want = []
+    reset()
+    for i in range(5):
+        between(i)
+        want.append([t.clone() for t in step()])
+    torch.cuda.synchronize()
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+        got = step()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        reset()
+        for i in range(5):
+            between(i)
+            g.replay()
+            for a, b in zip(got, want[i]):
+                assert torch.equal(a, b)
+    _ok(va)

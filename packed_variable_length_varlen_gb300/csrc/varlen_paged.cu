@@ -169,12 +169,9 @@ constexpr int kRowsWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kRowsWarps * 32)
-    varlen_paged_join_rows_kernel(const PagedParams p, const PagedParts parts, bool behind) {
+    varlen_paged_join_rows_kernel(const PagedParams p, const PagedParts parts) {
   __shared__ float weight[kRowsWarps][2 * kMaxSms];
-  // behind the other join, which waited for both kernels: only before it ends
-  // (the fence drops what this SM's L1 held before)
-  if (behind) __threadfence();
-  else dependency_wait();
+  dependency_wait();
   const PagedJoin u = parts.join[2 * blockIdx.x + 1];
   dependents_may_launch();
   if (u.parts != 0) {
@@ -186,7 +183,6 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
     if (t < half_tokens && tok < q1 - q0)
       join_by_warp<D>(p, parts, u, row, JoinRow{q0 + tok, u.kh * p.group + in_half - t * p.group}, weight[warp]);
   }
-  if (behind) dependency_wait();
 }
 
 template <int D>
@@ -196,8 +192,7 @@ cudaError_t launch_join_d(const PagedLaunch& L, cudaStream_t stream) {
     e = launch_overlapped(varlen_paged_join_kernel<D>,
                           dim3(L.sms * few_ctas(L.e4m3)), kJoinWarps * 32, 0, stream, L.p, L.few_parts);
   if (e == cudaSuccess && L.many)
-    e = launch_overlapped(varlen_paged_join_rows_kernel<D>, dim3(L.sms, kChunkRows / kRowsWarps), kRowsWarps * 32, 0, stream, L.p, L.chunk,
-                          L.few);
+    e = launch_overlapped(varlen_paged_join_rows_kernel<D>, dim3(L.sms, kChunkRows / kRowsWarps), kRowsWarps * 32, 0, stream, L.p, L.chunk);
   return e;
 }
 

@@ -174,8 +174,11 @@ inline PagedWorkspace paged_workspace(int64_t total_rows, int32_t head_dim) {  /
   return w;
 }
 
-// A kernel whose launch may begin while the one before it on the stream ends;
-// it waits (dependency_wait) before it touches memory.
+// A kernel whose launch may begin while the one before it on the stream ends.
+// Every thread of it waits (dependency_wait) before it touches global memory,
+// so that a grid ends only after all those before it on the stream: what any of
+// them wrote is complete where the wait returns.  (A kernel that skips the wait
+// has no claim to see anything, whatever waits stand in the grids before it.)
 template <class... P, class... A>
 cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
                               const A&... args) {

@@ -169,7 +169,7 @@ template <int D, bool E4M3>
 __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
     varlen_paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                             const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
-                            const PagedParams p, const PagedParts parts, int32_t take, bool behind) {
+                            const PagedParams p, const PagedParts parts, int32_t take) {
   using C = FewCfg<D, E4M3>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_addr(smem) & 1023u) != 0) {
@@ -191,12 +191,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
     sh.abort = 0;
     fence_barrier_init();
   }
-  // Nothing above reads or writes global memory.  Behind the kernel for many
-  // rows of the same call, which waited for what came before it, this one waits
-  // only before it ends: the two share nothing but their inputs.  What those
-  // kernels wrote is in L2 by then; the fence drops what this SM's L1 held before.
-  if (behind) __threadfence();
-  else dependency_wait();
+  dependency_wait();  // nothing above reads or writes global memory
   paged_start<typename C::Geom>(sh.start, p, take, kLeastTiles);
   dependents_may_launch();
   PagedWalk<typename C::Geom> walk;
@@ -654,7 +649,6 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
       }
     }
   }
-  if (behind) dependency_wait();
   __syncthreads();
   if (threadIdx.x == 0 && sh.abort) record_error(p.err, kErrTimeout);
 }
@@ -666,7 +660,7 @@ cudaError_t launch_few_d(const PagedLaunch& L, int32_t take, cudaStream_t stream
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_overlapped(kern, (unsigned)(L.sms * few_ctas(E4M3)), C::THREADS, C::SMEM, stream, L.few_k, L.few_v, L.few_ks,
-                           L.few_vs, L.p, L.few_parts, take, L.many);
+                           L.few_vs, L.p, L.few_parts, take);
 }
 
 }  // namespace

@@ -1,0 +1,38 @@
+"""Rules that the sources of the paged attention's kernels keep, read on the
+CPU: what they guard against (data read before it is complete) shows on a GPU
+as a wrong result once in a long while, if at all."""
+import pathlib
+import re
+
+CSRC = pathlib.Path(__file__).resolve().parents[1] / "packed_variable_length_varlen_gb300" / "csrc"
+KERNEL_FILES = ("varlen_paged.cu", "varlen_paged_few.cu", "varlen_paged_chunk.cu")
+
+
+def _source(name):
+    """The file's text without comments (role headings, `// ------ name`, are kept)."""
+    text = (CSRC / name).read_text()
+    return re.sub(r"//(?! ?-{4,}).*", "", text)
+
+
+def _kernels():
+    """(name, body) of every kernel that is launched to overlap with the one before it."""
+    for f in KERNEL_FILES:
+        text = _source(f)
+        for m in re.finditer(r"__global__ void[^{;]*?(varlen_paged_\w+_kernel)\([^{;]*\{", text):
+            body = text[m.end():]
+            yield m.group(1), body[:body.index("\n}\n")]
+
+
+def test_overlapped_kernels_wait_before_they_touch_memory():
+    """A grid that may start while the one before it on the stream still runs sees nothing of what that one (or any
+    before it) wrote until its own wait returns: each kernel waits once, whatever its arguments, before its first read."""
+    seen = []
+    for name, body in _kernels():
+        waits = [m.start() for m in re.finditer(r"dependency_wait\(\)", body)]
+        plain = [m.start() for m in re.finditer(r"^  dependency_wait\(\);", body, re.M)]
+        assert len(plain) == 1 and plain[0] + 2 == waits[-1], name
+        before = body[:plain[0]]
+        assert not re.search(r"__ldg|paged_start|paged_note|p\.(cu_q|pages|q\b|out|lse)|parts\.|tma_load", before), name
+        seen.append(name)
+    assert sorted(seen) == ["varlen_paged_chunk_kernel", "varlen_paged_few_kernel", "varlen_paged_join_kernel",
+                            "varlen_paged_join_rows_kernel"]

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   for (int which = 0; which < 2; ++which) {
     const PagedJoin u = units[which];
     if (u.parts == 0 || (which == 0 && u.parts <= kWarpParts)) continue;  // block-uniform
-    const int32_t q0 = clamp_row(__ldg(p.cu_q + u.b), p.total_q), q1 = clamp_row(__ldg(p.cu_q + u.b + 1), p.total_q);
+    const int32_t q0 = clamp_row(p.cu_q[u.b], p.total_q), q1 = clamp_row(p.cu_q[u.b + 1], p.total_q);
     const int32_t first = u.blk * p.few_rows, rows = min((q1 - q0) * p.group - first, p.few_rows);
     auto row_of = [&](int32_t row) {
       const int32_t tok = (first + row) / p.group;
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
   dependents_may_launch();
   if (u.parts != 0) {
     const int32_t warp = threadIdx.x >> 5, row = blockIdx.y * kRowsWarps + warp;
-    const int32_t q0 = clamp_row(__ldg(p.cu_q + u.b), p.total_q), q1 = clamp_row(__ldg(p.cu_q + u.b + 1), p.total_q);
+    const int32_t q0 = clamp_row(p.cu_q[u.b], p.total_q), q1 = clamp_row(p.cu_q[u.b + 1], p.total_q);
     const int32_t half_tokens = kChunkRows / 2 / p.group;
     const int32_t half = row >> 7, in_half = row & 127, t = in_half / p.group;
     const int64_t tok = (int64_t)u.blk * 2 * half_tokens + half * half_tokens + t;

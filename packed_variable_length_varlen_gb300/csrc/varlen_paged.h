@@ -23,6 +23,9 @@ Span checked_span(const void* base, int64_t bytes);
 Span nhd_bytes(const void* base, varlen_stride s, int64_t rows, int32_t H, int32_t D);
 
 // ------------------------------------------------- the cache
+// (Lengths, table, cu_seqlens and queries are read by ordinary loads: the
+// attention's kernels may start while earlier ones still write them, which the
+// non-coherent path does not allow.)
 struct PageView {
   const int32_t* table;
   int64_t table_stride;
@@ -33,14 +36,14 @@ struct PageView {
 // Positions sequence b holds, clamped to what its table row can name.
 __device__ __forceinline__ int32_t cache_len(const PageView& c, int32_t b) {
   const int64_t cap = (int64_t)c.max_pages << c.page_shift;
-  return (int32_t)min((int64_t)max(__ldg(c.seqlens + b), 0), cap);
+  return (int32_t)min((int64_t)max(c.seqlens[b], 0), cap);
 }
 
 // Page that holds positions [i << page_shift, ...) of sequence b, 0 <= i <
 // max_pages; num_pages (no page: recorded as an error) for an entry that
 // names none.
 __device__ __forceinline__ int32_t page_at(const PageView& c, int32_t b, int32_t i, unsigned int* err) {
-  const int32_t id = __ldg(c.table + (int64_t)b * c.table_stride + i);
+  const int32_t id = c.table[(int64_t)b * c.table_stride + i];
   if ((uint32_t)id < (uint32_t)c.num_pages) return id;
   if (err != nullptr) atomicOr(err, (unsigned int)kErrBounds);
   return c.num_pages;
@@ -53,7 +56,7 @@ __device__ __forceinline__ int32_t warp_find_segment(const int32_t* cu, int32_t 
   while (hi - lo > 1) {
     const int32_t step = (hi - lo + 31) / 32;
     const int64_t i = (int64_t)lo + (int64_t)(threadIdx.x & 31) * step;
-    const bool below = i < hi && clamp_row(__ldg(cu + i), total) <= row;
+    const bool below = i < hi && clamp_row(cu[i], total) <= row;
     const unsigned m = __ballot_sync(0xffffffffu, below);
     const int32_t k = m == 0 ? 0 : 31 - __clz(m);
     lo += k * step;

@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
         const __nv_bfloat16* qa =
             p.q + (int64_t)(x.q0 + x.u.t0 + t) * p.q_rs + (int64_t)(x.kh * p.group + at - t * p.group) * p.q_hs;
         auto load = [&](int d0) {
-          return live && d0 < D && in_span(p.q_span, qa + d0, 16, p.err) ? __ldg(reinterpret_cast<const uint4*>(qa + d0))
+          return live && d0 < D && in_span(p.q_span, qa + d0, 16, p.err) ? *reinterpret_cast<const uint4*>(qa + d0)
                                                                         : make_uint4(0, 0, 0, 0);
         };
 #pragma unroll

@@ -66,7 +66,7 @@ struct PagedGeom {
 template <class G>
 __device__ __forceinline__ PagedSeg paged_seg(const PagedParams& p, int32_t b, int32_t take) {
   PagedSeg s;
-  const int32_t a = clamp_row(__ldg(p.cu_q + b), p.total_q), e = clamp_row(__ldg(p.cu_q + b + 1), p.total_q);
+  const int32_t a = clamp_row(p.cu_q[b], p.total_q), e = clamp_row(p.cu_q[b + 1], p.total_q);
   s.q0 = a;
   s.n = max(e - a, 0);
   s.sk = cache_len(p.pages, b);

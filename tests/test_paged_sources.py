@@ -36,3 +36,10 @@ def test_overlapped_kernels_wait_before_they_touch_memory():
         seen.append(name)
     assert sorted(seen) == ["varlen_paged_chunk_kernel", "varlen_paged_few_kernel", "varlen_paged_join_kernel",
                             "varlen_paged_join_rows_kernel"]
+
+
+def test_overlapped_kernels_read_with_ordinary_loads():
+    """The non-coherent path (__ldg, ld.global.nc) is for data that nobody writes while the kernel lives; a kernel that
+    started early lives while the ones before it still write the lengths, the table and the queries."""
+    for f in KERNEL_FILES + ("varlen_paged_walk.cuh", "varlen_paged.h"):
+        assert not re.search(r"__ldg|__ldlu|ld\.global\.nc|__restrict__", _source(f)), f

@@ -72,6 +72,7 @@ __device__ __forceinline__ void join_by_warp(const PagedParams& p, const PagedPa
   for (int i = 0; i < D / 32; ++i)
     if (in_span(p.out_span, a + i * 32, 2, p.err)) a[i * 32] = __float2bfloat16_rn(o[i] * inv);
   if (lane == 0) join_lse(p, r, m, l);
+  __syncwarp();  // a warp's next row writes the weights that all its lanes read here
 }
 
 // The sum (or maximum) of v over the block, in a fixed order.

@@ -43,3 +43,13 @@ def test_overlapped_kernels_read_with_ordinary_loads():
     started early lives while the ones before it still write the lengths, the table and the queries."""
     for f in KERNEL_FILES + ("varlen_paged_walk.cuh", "varlen_paged.h"):
         assert not re.search(r"__ldg|__ldlu|ld\.global\.nc|__restrict__", _source(f)), f
+
+
+def test_a_warp_parts_its_rows_in_the_join():
+    """A warp joins row after row through the same weights in shared memory: it comes together after the last read of
+    one row's (the divergent store of the row's LSE is no meeting point) and before the first write of the next one's."""
+    text = _source("varlen_paged.cu")
+    body = text[text.index("void join_by_warp("):]
+    body = body[:body.index("\n}\n")]
+    assert body.rstrip().endswith("__syncwarp();")
+    assert body.index("weight[2 * k] = ex2") < body.index("__syncwarp();") < body.index("fmaf(oa")

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
   using C = ChunkCfg<D, E4M3>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_addr(smem) & 1023u) != 0) {
-    if (threadIdx.x == 0) record_error(p.err, kErrBounds);
+    paged_refuse(p, parts);
     return;
   }
   ChunkShared& sh = *reinterpret_cast<ChunkShared*>(smem);

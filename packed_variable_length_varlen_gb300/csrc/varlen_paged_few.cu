@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
   using C = FewCfg<D, E4M3>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_addr(smem) & 1023u) != 0) {
-    if (threadIdx.x == 0) record_error(p.err, kErrBounds);
+    paged_refuse(p, parts);
     return;
   }
   FewShared& sh = *reinterpret_cast<FewShared*>(smem);

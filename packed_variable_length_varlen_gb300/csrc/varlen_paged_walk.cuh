@@ -19,6 +19,7 @@
 // per thread) and finds where its part begins.
 #pragma once
 
+#include "sm103_ptx.cuh"
 #include "varlen_paged.h"
 
 namespace varlen {
@@ -261,6 +262,15 @@ struct PagedWalk {
     return true;
   }
 };
+
+// A CTA that cannot work: an error, and no unit for the join (which would take
+// what the workspace happens to hold for one).
+__device__ __forceinline__ void paged_refuse(const PagedParams& p, const PagedParts& parts) {
+  dependency_wait();
+  if (threadIdx.x != 0) return;
+  parts.join[2 * blockIdx.x].parts = parts.join[2 * blockIdx.x + 1].parts = 0;
+  record_error(p.err, kErrBounds);
+}
 
 // Left for the join by the one thread that calls it, for every piece: the
 // units that the CTA holds a part of (its first and its last piece, if any).

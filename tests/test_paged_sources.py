@@ -53,3 +53,15 @@ def test_a_warp_parts_its_rows_in_the_join():
     body = body[:body.index("\n}\n")]
     assert body.rstrip().endswith("__syncwarp();")
     assert body.index("weight[2 * k] = ex2") < body.index("__syncwarp();") < body.index("fmaf(oa")
+
+
+def test_a_kernel_that_returns_early_leaves_the_join_nothing():
+    """The workspace holds anything on entry and the join follows what it finds there: a CTA that gives up before its
+    producer cleared its entries clears them itself (after the wait)."""
+    for name, body in _kernels():
+        for m in re.finditer(r"^ {2,}return;", body, re.M):
+            assert body[:m.start()].rstrip().endswith("paged_refuse(p, parts);"), name
+    walk = _source("varlen_paged_walk.cuh")
+    body = walk[walk.index("void paged_refuse("):]
+    body = body[:body.index("\n}\n")]
+    assert body.index("dependency_wait();") < body.index("parts = 0;") < body.index("record_error")

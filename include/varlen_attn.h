@@ -574,7 +574,9 @@ int varlen_attn_debug_set_span_slack(int64_t bytes);
  * Failure test of the bounded waits: with which = 0 the K/V producer of the
  * forward's CTA 0 leaves out its load number n (0-based, K and V loads
  * counted alike); with which = 1 the Q producer of the backward's CTA 0
- * leaves out the Q load of its step n.  The waits for that load give up
+ * leaves out the Q load of its step n; with which = 3 (the paged attention's
+ * kernel for few rows) or 4 (the one for many) the producer of CTA 0 leaves
+ * out its K/V load number n.  The waits for that load give up
  * after their budget (2 s), every role of the CTA unwinds (the producer
  * waits, bounded, for its copies in flight; the MMA issuer drains its
  * products; TMEM is freed) and varlen_attn_get_device_status returns

@@ -90,6 +90,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   return false;
 }
 
+// mbar_wait by a whole warp, its outcome the same in every lane: a lane that
+// gives up takes the others with it, so that none is left behind at the warp's
+// next common instruction.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
 // Re-balance registers between warpgroups (all four warps of a warpgroup
 // execute the same instruction).  The block launches with its compiled
 // per-thread count LAUNCH; a warpgroup moving to N registers must use the

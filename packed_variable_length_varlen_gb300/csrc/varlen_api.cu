@@ -246,10 +246,10 @@ cudaEvent_t g_phase_events[4] = {nullptr, nullptr, nullptr, nullptr};
 std::mutex g_phase_mu;
 
 // Debug knobs (process-wide): bytes taken off every operand span (the
-// bounds checker's self test) and the load the forward / backward producer
-// of CTA 0 leaves out (the failure test).
+// bounds checker's self test) and the load that a kernel's producer in CTA 0
+// leaves out (the failure test).
 std::atomic<int64_t> g_span_slack{0};
-std::atomic<int64_t> g_skip_fwd_load{-1}, g_skip_bwd_step{-1};
+std::atomic<int64_t> g_skip_fwd_load{-1}, g_skip_bwd_step{-1}, g_skip_paged_few{-1}, g_skip_paged_many{-1};
 
 // Bytes an NHD operand of `rows` rows occupies from its base: up to the end
 // of its last (row, head) vector.
@@ -325,6 +325,11 @@ int encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const voi
                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                    promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? VARLEN_OK : VARLEN_ERR_STRIDE;
+}
+
+void paged_skip_knobs(int32_t* few, int32_t* many) {
+  *few = skip_knob(g_skip_paged_few);
+  *many = skip_knob(g_skip_paged_many);
 }
 
 Span checked_span(const void* base, int64_t bytes) { return flat_span(base, bytes); }
@@ -935,6 +940,8 @@ extern "C" int varlen_attn_debug_set_span_slack(int64_t bytes) {
 extern "C" int varlen_attn_debug_skip_load(int which, int64_t n) {
   if (which == 0) g_skip_fwd_load.store(n < 0 ? -1 : n);
   else if (which == 1) g_skip_bwd_step.store(n < 0 ? -1 : n);
+  else if (which == 3) g_skip_paged_few.store(n < 0 ? -1 : n);
+  else if (which == 4) g_skip_paged_many.store(n < 0 ? -1 : n);
   else return VARLEN_ERR_SHAPE;
   return VARLEN_OK;
 }

@@ -17,6 +17,8 @@ int check_nhd(const void* ptr, varlen_stride s, int64_t rows, int32_t H, int32_t
 // A tiled tensor map of `rank` dimensions (128-byte swizzle or none), 64-bit extents.
 int encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
                  const cuuint64_t* byte_strides, const cuuint32_t* box, bool swizzle);
+// Loads that the producers of CTA 0 leave out (failure test; < 0: none).
+void paged_skip_knobs(int32_t* few, int32_t* many);
 // [base, base + bytes), shortened by the bounds checker's self test.
 Span checked_span(const void* base, int64_t bytes);
 // The bytes an NHD bf16 operand occupies.
@@ -104,6 +106,7 @@ struct PagedParams {
   int64_t win_left, win_right;
   float scale_log2;
   unsigned int* err;
+  int32_t debug_skip_few, debug_skip_many;  // < 0: off; else CTA 0's producer skips its load number n (failure test)
   Span q_span, out_span, lse_span, kp_span, vp_span, ks_span, vs_span;  // bounds-checking build
 };
 

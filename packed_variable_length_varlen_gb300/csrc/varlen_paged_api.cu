@@ -241,6 +241,7 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   p.win_right = window_right < 0 ? kWinUnbounded : window_right;
   p.scale_log2 = scale * kLog2e;
   p.err = err;
+  paged_skip_knobs(&p.debug_skip_few, &p.debug_skip_many);
   p.q_span = nhd_bytes(q, sq, total_q, num_heads, c.head_dim);
   p.out_span = nhd_bytes(out, so, total_q, num_heads, c.head_dim);
   p.lse_span = checked_span(lse, (int64_t)num_heads * total_q * 4);

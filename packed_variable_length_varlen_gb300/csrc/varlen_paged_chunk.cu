@@ -81,11 +81,13 @@ struct ChunkShared {
 static_assert(sizeof(ChunkShared) <= 1024, "barrier block too large");
 
 // The next piece from the ring (b < 0: there is none); false on giving up.
+// WARP: a whole warp reads it, and gives up as one; else a single thread does.
+template <bool WARP>
 struct PieceReader {
   uint32_t n = 0;
   __device__ __forceinline__ bool next(ChunkShared& sh, PagedPiece& x, volatile int* abort) {
-    const uint32_t i = n % kPieces;
-    if (!mbar_wait(&sh.piece_full[i], (n / kPieces) & 1, abort)) return false;
+    const uint32_t i = n % kPieces, parity = (n / kPieces) & 1;
+    if (!(WARP ? mbar_wait_warp(&sh.piece_full[i], parity, abort) : mbar_wait(&sh.piece_full[i], parity, abort))) return false;
     x = sh.piece[i];
     mbar_arrive(&sh.piece_empty[i]);
     ++n;
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         const bool more = walk.next(p, x);
         if (!more) x.b = -1;
         const uint32_t slot = handed % kPieces;
-        if (!mbar_wait(&sh.piece_empty[slot], ((handed / kPieces) & 1) ^ 1, abort)) {
+        if (!mbar_wait_warp(&sh.piece_empty[slot], ((handed / kPieces) & 1) ^ 1, abort)) {
           ok = false;
           break;
         }
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         if (!more) break;
         const int32_t tiles = min(x.j1, x.u.tiles);
         if (x.j0 >= tiles) continue;  // no key: nothing to load
-        if (q_loads > 0 && !mbar_wait(&sh.q_empty, (q_loads - 1) & 1, abort)) {
+        if (q_loads > 0 && !mbar_wait_warp(&sh.q_empty, (q_loads - 1) & 1, abort)) {
           ok = false;
           break;
         }
@@ -219,10 +221,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
 #pragma unroll
           for (int which = 0; which < 2; ++which, ++pos) {
             const uint32_t s = pos % kRing;
-            if (!mbar_wait(&empty[s], ((pos / kRing) & 1) ^ 1, abort)) {
+            if (!mbar_wait_warp(&empty[s], ((pos / kRing) & 1) ^ 1, abort)) {
               ok = false;
               break;
             }
+            // (failure test: CTA 0 leaves one load out)
+            if (blockIdx.x == 0 && (int64_t)pos == (int64_t)p.debug_skip_many) continue;
             if (lane == 0) mbar_arrive_expect_tx(&full[s], E4M3 ? C::CHUNK + kChunkTile * 2 : C::TILE);
             __syncwarp();
             uint8_t* dst = (E4M3 ? raw + s * C::CHUNK : ring + s * C::TILE) + cc * C::CHUNK + (piece << box_shift) * 128;
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                         kIdescO, (!first || kk > 0) ? 1u : 0u);
           mma_commit(&sh.pv_done[hf]);
         };
-        PieceReader pieces;
+        PieceReader<false> pieces;
         PagedPiece x;
         uint32_t q_loads = 0, pos = 0, g[2] = {0, 0};  // steps of each half so far
         bool ok = true;
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
       }
     } else if constexpr (!E4M3) {
       // ---------------------------------------------------------- clearing (bf16)
-      PieceReader pieces;
+      PieceReader<true> pieces;
       PagedPiece x;
       uint32_t pos = 0;
       bool ok = true;
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         const int32_t tiles = min(x.j1, x.u.tiles);
         for (int32_t j = x.j0; j < tiles; ++j, pos += 2) {
           const uint32_t vpos = pos + 1, s = vpos % C::NSLOT;
-          if (!mbar_wait(&sh.kv_full[s], (vpos / C::NSLOT) & 1, abort)) { ok = false; break; }
+          if (!mbar_wait_warp(&sh.kv_full[s], (vpos / C::NSLOT) & 1, abort)) { ok = false; break; }
           const int32_t key0 = (x.u.tile0 + j) * kChunkTile;
           const int lo = max(x.u.lo - key0, 0), hi = min(x.u.hi - key0, kChunkTile);
           if (lo > 0 || hi < kChunkTile) {
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
     const uint32_t s_col = hf * 128, o_col = C::O_COL + hf * 128;
     const float c2 = p.scale_log2;
     const int32_t row_tok = row / p.group, row_head = row - row_tok * p.group;
-    PieceReader pieces;
+    PieceReader<true> pieces;
     PagedPiece x;
     uint32_t g = 0;
     bool ok = true;
@@ -372,7 +376,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
       if (live) band_keys(tok, tok, x.n, x.sk, p.win_left, p.win_right, &key_lo, &key_hi);
       const int32_t key0 = (x.u.tile0 + x.j0) * kChunkTile;
       for (int32_t j = 0; j < tiles; ++j) {
-        if (!mbar_wait(&sh.s_full[hf], (g + j) & 1, abort)) { ok = false; break; }
+        if (!mbar_wait_warp(&sh.s_full[hf], (g + j) & 1, abort)) { ok = false; break; }
         tc_fence_after();
         uint32_t s[128];
         {
@@ -459,7 +463,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
       const bool whole = x.whole();
       float* part = parts.o + ((2 * (int64_t)blockIdx.x + (x.begins() ? 1 : 0)) * parts.rows + hf * 128 + row) * D;
       if (tiles > 0) {
-        if (!mbar_wait(&sh.pv_done[hf], (g + tiles - 1) & 1, abort)) break;
+        if (!mbar_wait_warp(&sh.pv_done[hf], (g + tiles - 1) & 1, abort)) break;
         tc_fence_after();
       }
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no key: 0; NaN stays
@@ -509,7 +513,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
     const int t = threadIdx.x - 384;  // 0..127
     const int cc = C::NC == 2 ? t >> 6 : 0, r0 = C::NC == 2 ? t & 63 : t;
     const int box_shift = min(p.pages.page_shift, 7);
-    PieceReader pieces;
+    PieceReader<true> pieces;
     PagedPiece x;
     uint32_t pos = 0;
     bool ok = true;
@@ -520,8 +524,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
 #pragma unroll 1
         for (int which = 0; which < 2; ++which, ++pos) {
           const uint32_t rs = pos % C::NRAW, s = pos % C::NSLOT;
-          if (!mbar_wait(&sh.raw_full[rs], (pos / C::NRAW) & 1, abort)) { ok = false; break; }
-          if (!mbar_wait(&sh.kv_empty[s], ((pos / C::NSLOT) & 1) ^ 1, abort)) { ok = false; break; }
+          if (!mbar_wait_warp(&sh.raw_full[rs], (pos / C::NRAW) & 1, abort)) { ok = false; break; }
+          if (!mbar_wait_warp(&sh.kv_empty[s], ((pos / C::NSLOT) & 1) ^ 1, abort)) { ok = false; break; }
           __syncwarp();
           const uint8_t* src = raw + rs * C::CHUNK;
           const uint8_t* sc = scales + rs * C::SCALES;

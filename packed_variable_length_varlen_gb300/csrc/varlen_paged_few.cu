@@ -117,8 +117,8 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-// mbar_wait by a whole warp, its outcome the same in every lane.  The loop
-// stands apart, so that the way through a tile stays short.
+// mbar_wait_warp whose loop stands apart, so that the way through a tile stays
+// short.
 __device__ __noinline__ bool warp_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
@@ -223,10 +223,12 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
 #pragma unroll
         for (int which = 0; which < 2; ++which, ++pos) {
           const uint32_t slot = pos % C::NSLOT;
-          if (!mbar_wait(&sh.empty[slot], ((pos / C::NSLOT) & 1) ^ 1, abort)) {
+          if (!mbar_wait_warp(&sh.empty[slot], ((pos / C::NSLOT) & 1) ^ 1, abort)) {
             ok = false;
             break;
           }
+          // (failure test: CTA 0 leaves one load out)
+          if (blockIdx.x == 0 && (int64_t)pos == (int64_t)p.debug_skip_few) continue;
           if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], C::TILE + (E4M3 ? C::KT * 2 : 0));
           __syncwarp();
           if (loads)
@@ -238,7 +240,6 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
         }
       }
     }
-    ok = __all_sync(0xffffffffu, ok);
     if (!ok && lane == 0) {
       // every copy in flight lands before the CTA's shared memory is released (bounded)
       for (uint32_t s = 0; s < C::NSLOT && s < pos; ++s) {

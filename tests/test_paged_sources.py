@@ -1,6 +1,7 @@
 """Rules that the sources of the paged attention's kernels keep, read on the
-CPU: what they guard against (data read before it is complete) shows on a GPU
-as a wrong result once in a long while, if at all."""
+CPU: what they guard against (data read before it is complete, a warp that
+parts at a wait) shows on a GPU as a wrong result or a hang once in a long
+while, if at all."""
 import pathlib
 import re
 
@@ -65,3 +66,21 @@ def test_a_kernel_that_returns_early_leaves_the_join_nothing():
     body = walk[walk.index("void paged_refuse("):]
     body = body[:body.index("\n}\n")]
     assert body.index("dependency_wait();") < body.index("parts = 0;") < body.index("record_error")
+
+
+def test_a_wait_that_can_give_up_has_one_outcome_for_a_warp():
+    """Every wait whose failure makes a role leave is voted on by the whole warp (mbar_wait_warp, warp_wait), but for
+    the product issuer's, which is one thread: lanes that leave one by one would leave the others at the warp's next
+    __syncwarp."""
+    few = _source("varlen_paged_few.cu")
+    assert not re.findall(r"!\s*mbar_wait\(", few)
+    roles = re.split(r"// -{4,} (.*)", _source("varlen_paged_chunk.cu"))
+    names = [r.strip() for r in roles[1::2]]
+    assert names == ["producer", "MMA issuer", "clearing (bf16)", "softmax", "codes to bf16"]
+    for name, body in zip(names, roles[2::2]):
+        alone, voted = re.findall(r"!\s*mbar_wait\(", body), re.findall(r"!\s*mbar_wait_warp\(", body)
+        reader = re.findall(r"PieceReader<(\w+)>", body)
+        if name == "MMA issuer":
+            assert alone and not voted and reader == ["false"]
+        else:
+            assert voted and not alone and reader in ([], ["true"]), name

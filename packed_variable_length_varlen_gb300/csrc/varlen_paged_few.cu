@@ -40,12 +40,18 @@
 //   S: a row of Q is multiplied by the power of two that brings its largest
 //      element to 2^14 (f16 then holds all of a bf16 that is not 2^-28 of the
 //      largest), and S by that power's inverse and the key's scale.
-//   P V: the weight of key j is P_j s_j / R * 2^7, with R the largest scale
-//      that the warp has met (o is kept in units of R 2^-7): at most 2^15, and
-//      f16's 11 bits hold down to 2^-21 of the largest term.  Where a key's
-//      scale lies more than 2^12 below R (or is NaN), the step's products run
-//      in bf16 instead: a code's bits s eeee mmm moved to s 0000eeee mmm0000 are
-//      the bf16 code * 2^-120, subnormals too, times 2^127 s / R.
+//   P V: the weight of key j is P_j s_j / R * 2^13, with R the largest scale
+//      that the warp has met (o is kept in units of R 2^-13): at most 2^15, as P
+//      stays below 2^2 (the maximum follows when a key passes it by more), and
+//      f16 holds it in 11 bits down to P_j s_j / R = 2^-27, as well as bf16 would
+//      down to 2^-29, and with an error of 2^-38 below.  Where a key's scale lies
+//      more than 2^8 below R (or is NaN), the step's products run in bf16
+//      instead, so that P_j is held to bf16's 8 bits or better down to 2^-21 of
+//      the row's largest weight whatever the scales are: a code's bits s eeee mmm
+//      moved to s 0000eeee mmm0000 are the bf16 code * 2^-120, subnormals too,
+//      times 2^127 s / R, and P times 2^6.  A vector of zeros has a scale of 1
+//      that says nothing of its neighbours' size: it counts as one that is not
+//      there, and R does not follow it.
 #include <cuda_fp8.h>
 
 #include "sm103_ptx.cuh"
@@ -395,11 +401,12 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
                 s[e] = key >= klo[e & 1] && key < khi[e & 1] ? s[e] : -INFINITY;
               }
             }
-            // The maximum follows only when a key passes it by more than 2^8 (o and l
-            // carry the same factor, so nothing is lost): the lanes of a row need to
-            // look at one another's keys only then.
+            // The maximum follows only when a key passes it by more than 2^8, with E4M3
+            // 2^2 (o and l carry the same factor, so nothing is lost): the lanes of a
+            // row need to look at one another's keys only then.
+            constexpr float kLag = E4M3 ? 2.f : 8.f;
             float mx[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
-            if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+            if (__any_sync(0xffffffffu, mx[0] > m[0] + kLag || mx[1] > m[1] + kLag)) {
 #pragma unroll
               for (int w = 4; w < 32; w <<= 1) {
                 mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], w));
@@ -475,12 +482,37 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
               }
             }
             auto odd = [&] {
-              const float least = vref * 0x1p-12f;
+              const float least = vref * 0x1p-8f;
               return __any_sync(0xffffffffu, !(sv[0] <= vref) || !(sv[1] <= vref) || (sv[0] < least && sv[0] != 0.f) ||
                                                  (sv[1] < least && sv[1] != 0.f));
             };
             bool wide = odd();
-            if (wide) {  // a new largest scale: o to its units; and look again
+            if (wide) {
+              // Vectors of zeros (with a finite scale) drop out: bit k of `here` says
+              // that key 2c + (k & 1) + 8 (k >> 1) has a code that is not zero, then
+              // each lane asks for the keys of its scales, and tells which drop.
+              uint32_t here = 0;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t any = 0;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) any |= w[k][i];
+                here |= (any & 0x7f7f7f7fu) != 0 ? 1u << k : 0u;
+              }
+#pragma unroll
+              for (int k = 4; k < 32; k <<= 1) here |= __shfl_xor_sync(0xffffffffu, here, k);
+              here = __shfl_sync(0xffffffffu, here, r >> 1) >> (r & 1);
+              uint32_t drop = 0;  // bit 0: key a + r, bit 1: a + r + 8
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                if (((here >> (2 * k)) & 1u) == 0 && sv[k] == sv[k]) {
+                  sv[k] = 0.f;
+                  drop |= 1u << k;
+                }
+              const uint32_t d0 = __shfl_sync(0xffffffffu, drop, 8 * c), d1 = __shfl_sync(0xffffffffu, drop, 8 * c + 4);
+              keep0 &= ((d0 & 1u) ? 0u : 0xffffu) | ((d1 & 1u) ? 0u : 0xffff0000u);
+              keep1 &= ((d0 & 2u) ? 0u : 0xffffu) | ((d1 & 2u) ? 0u : 0xffff0000u);
+              // a new largest scale: o to its units; and look again
               float top = fmaxf(sv[0], sv[1]);
 #pragma unroll
               for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
@@ -492,11 +524,11 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
                 for (int t = 0; t < C::MT; ++t)
 #pragma unroll
                   for (int e = 0; e < 4; ++e) o[t][e] *= f;
-                wide = odd();
               }
+              wide = odd();
             }
             if (!wide) {
-              const float f0 = sv[0] * vinv * 0x1p7f, f1 = sv[1] * vinv * 0x1p7f;
+              const float f0 = sv[0] * vinv * 0x1p13f, f1 = sv[1] * vinv * 0x1p13f;
               const uint32_t p0 = transpose8(pack_f16x2(s[0] * f0, s[1] * f0));
               const uint32_t p1 = transpose8(pack_f16x2(s[2] * f1, s[3] * f1));
 #pragma unroll
@@ -518,7 +550,8 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
                 const uint32_t sc = lds<uint32_t>(vsc + scale_at(a + 2 * c + 8 * k, box_shift)) & (k ? keep1 : keep0);
                 f[k] = pack_bf16x2(bf16_lo(sc) * up * 0x1p127f, bf16_hi(sc) * up * 0x1p127f);
               }
-              const uint32_t p0 = transpose8(pack_bf16x2(s[0], s[1])), p1 = transpose8(pack_bf16x2(s[2], s[3]));
+              const uint32_t p0 = transpose8(pack_bf16x2(s[0] * 0x1p6f, s[1] * 0x1p6f));
+              const uint32_t p1 = transpose8(pack_bf16x2(s[2] * 0x1p6f, s[3] * 0x1p6f));
 #pragma unroll
               for (int t = 0; t < C::MT; ++t) {
                 uint32_t b[4];
@@ -548,7 +581,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
       }
       if (!ok) break;
       if constexpr (E4M3) {
-        const float f = vref * 0x1p-7f;
+        const float f = vref * 0x1p-13f;
 #pragma unroll
         for (int t = 0; t < C::MT; ++t)
 #pragma unroll

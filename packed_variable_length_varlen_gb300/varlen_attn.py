@@ -604,7 +604,8 @@ class PagedCache:
 
     The tensors are kept, not copied: what a program writes into them (a new
     page in the table, longer seqlens) is seen by later calls.  ``struct`` is
-    the C description of them.
+    the C description of them: their addresses, so they stay where they are
+    (no resize_ or set_), and another tensor in the place of one is refused.
     """
 
     def __init__(self, k_pages, v_pages, block_table, seqlens, k_scale=None, v_scale=None):
@@ -644,6 +645,13 @@ class PagedCache:
         c.num_pages, c.page_size, c.num_kv_heads, c.head_dim = pages, page_size, heads, dim
         c.max_pages = block_table.shape[1]
         self.struct, self.ref = c, ctypes.byref(c)
+
+    def __setattr__(self, name, value):
+        # set once: calls use the struct, which another value here would not reach (the same tensor again is what
+        # `cache.seqlens += n` assigns)
+        if name in self.__dict__ and self.__dict__[name] is not value:
+            raise AttributeError("PagedCache.%s is fixed: write into the tensor, or make another PagedCache" % name)
+        object.__setattr__(self, name, value)
 
 
 def _packed(cache, t, heads, rows=None):

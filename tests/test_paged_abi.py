@@ -203,3 +203,23 @@ def test_the_binding_refuses_calls(va):
     for kw in ({"out": q[:3]}, {"out": q.float()}, {"lse": torch.zeros(4, 3)}, {"lse": torch.zeros(4, 4).double()}):
         with pytest.raises(ValueError):
             va.attention_fwd_paged(q, c, cu, **kw)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_the_handle_refuses_other_tensors(va, kind):
+    """Calls use what the handle was made with: another tensor in its place would be without effect and is refused;
+    writing into the ones it has (`+=` among the ways) is not."""
+    t = _tensors(kind)
+    c = va.PagedCache(**t)
+    for name in ("k_pages", "v_pages", "block_table", "seqlens", "k_scale", "v_scale"):
+        old = getattr(c, name)
+        with pytest.raises(AttributeError, match=name):
+            setattr(c, name, torch.zeros(1) if old is None else old.clone())
+        assert getattr(c, name) is old
+    for name in ("batch", "num_kv_heads", "head_dim", "device", "struct"):
+        with pytest.raises(AttributeError, match=name):
+            setattr(c, name, 1)
+    c.seqlens += 3
+    c.block_table[0, 1] = 5
+    assert t["seqlens"].tolist() == [3, 3, 3] and int(t["block_table"][0, 1]) == 5
+    assert c.struct.seqlens == t["seqlens"].data_ptr()

@@ -34,6 +34,15 @@ __device__ __forceinline__ void join_lse(const PagedParams& p, const JoinRow& r,
 }
 __device__ __forceinline__ float join_inv(float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); }  // no key: 0; NaN stays
 
+// (m, l) of slot row i, and an element of its output, as a part left them.
+__device__ __forceinline__ float2 part_ml(const PagedParams& p, const PagedParts& parts, int64_t i) {
+  const float* a = parts.ml + 2 * i;
+  return in_span(parts.ml_span, a, 8, p.err) ? *reinterpret_cast<const float2*>(a) : make_float2(-INFINITY, 0.f);
+}
+__device__ __forceinline__ float part_o(const PagedParams& p, const PagedParts& parts, const float* a) {
+  return in_span(parts.o_span, a, 4, p.err) ? *a : 0.f;
+}
+
 // One warp joins slot row `row` of unit u.
 template <int D>
 __device__ __forceinline__ void join_by_warp(const PagedParams& p, const PagedParts& parts, const PagedJoin& u,
@@ -42,7 +51,7 @@ __device__ __forceinline__ void join_by_warp(const PagedParams& p, const PagedPa
   auto at = [&](int32_t k) { return (2 * (int64_t)(u.first + k) + (k == 0 ? 1 : 0)) * parts.rows + row; };
   float m = -INFINITY, l = 0.f;
   for (int32_t k = lane; k < u.parts; k += 32) {
-    const float2 ml = *reinterpret_cast<const float2*>(parts.ml + at(k) * 2);
+    const float2 ml = part_ml(p, parts, at(k));
     weight[2 * k] = ml.x;
     weight[2 * k + 1] = ml.y;
     m = fmaxf(m, ml.x);
@@ -64,7 +73,7 @@ __device__ __forceinline__ void join_by_warp(const PagedParams& p, const PagedPa
   for (int32_t k = 0; k < u.parts; ++k) {
     const float* oa = parts.o + at(k) * D + lane;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = fmaf(oa[i * 32], weight[2 * k], o[i]);
+    for (int i = 0; i < D / 32; ++i) o[i] = fmaf(part_o(p, parts, oa + i * 32), weight[2 * k], o[i]);
   }
   const float inv = join_inv(l);
   __nv_bfloat16* a = p.out + r.q * p.o_rs + (int64_t)r.head * p.o_hs + lane;
@@ -99,7 +108,7 @@ __device__ __forceinline__ void join_by_block(const PagedParams& p, const PagedP
   auto at = [&](int32_t k) { return (2 * (int64_t)(u.first + k) + (k == 0 ? 1 : 0)) * parts.rows + row; };
   float m = -INFINITY;
   for (int32_t k = threadIdx.x; k < u.parts; k += kJoinWarps * 32) {
-    const float2 ml = *reinterpret_cast<const float2*>(parts.ml + at(k) * 2);
+    const float2 ml = part_ml(p, parts, at(k));
     weight[2 * k] = ml.x;
     weight[2 * k + 1] = ml.y;
     m = fmaxf(m, ml.x);
@@ -119,7 +128,7 @@ __device__ __forceinline__ void join_by_block(const PagedParams& p, const PagedP
   for (int32_t k = warp; k < u.parts; k += kJoinWarps) {
     const float* oa = parts.o + at(k) * D + lane;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = fmaf(oa[i * 32], weight[2 * k], o[i]);
+    for (int i = 0; i < D / 32; ++i) o[i] = fmaf(part_o(p, parts, oa + i * 32), weight[2 * k], o[i]);
   }
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) so[warp][i * 32 + lane] = o[i];
@@ -139,7 +148,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     varlen_paged_join_kernel(const PagedParams p, const PagedParts parts) {
   __shared__ float so[kJoinWarps][D], weight[2 * kMaxParts], tmp[kJoinWarps];
   dependency_wait();
-  const PagedJoin units[2] = {parts.join[2 * blockIdx.x], parts.join[2 * blockIdx.x + 1]};
+  const PagedJoin units[2] = {get_join(p, parts, 2 * blockIdx.x), get_join(p, parts, 2 * blockIdx.x + 1)};
   dependents_may_launch();
   const int warp = threadIdx.x >> 5;
 #pragma unroll 1
@@ -173,7 +182,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
     varlen_paged_join_rows_kernel(const PagedParams p, const PagedParts parts) {
   __shared__ float weight[kRowsWarps][2 * kMaxSms];
   dependency_wait();
-  const PagedJoin u = parts.join[2 * blockIdx.x + 1];
+  const PagedJoin u = get_join(p, parts, 2 * blockIdx.x + 1);
   dependents_may_launch();
   if (u.parts != 0) {
     const int32_t warp = threadIdx.x >> 5, row = blockIdx.y * kRowsWarps + warp;

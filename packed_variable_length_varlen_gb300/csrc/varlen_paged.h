@@ -96,18 +96,15 @@ struct PagedParams {
   __nv_bfloat16* out;
   int64_t o_rs, o_hs;
   float* lse;
-  const uint8_t *k, *v;
-  int64_t k_page, k_row, k_head, v_page, v_row, v_head;  // byte strides of the pages
-  const __nv_bfloat16 *k_scale, *v_scale;
-  PageView pages;
+  PageView pages;  // (keys, values and scales are read by TMA alone)
   const int32_t* cu_q;
-  int32_t batch, total_q, num_heads, kv_heads, group;
+  int32_t batch, total_q, kv_heads, group;
   int32_t few_rows;  // up to which the kernel for few rows takes a segment
   int64_t win_left, win_right;
   float scale_log2;
   unsigned int* err;
   int32_t debug_skip_few, debug_skip_many;  // < 0: off; else CTA 0's producer skips its load number n (failure test)
-  Span q_span, out_span, lse_span, kp_span, vp_span, ks_span, vs_span;  // bounds-checking build
+  Span q_span, out_span, lse_span;  // bounds-checking build
 };
 
 // What a kernel takes: segments of at most few_rows() rows, of more, or all.
@@ -141,6 +138,7 @@ struct PagedParts {
   float* ml;
   PagedJoin* join;
   int32_t rows;  // rows of a slot
+  Span o_span, ml_span, join_span;  // bounds-checking build
 };
 
 struct PagedLaunch {
@@ -156,14 +154,18 @@ struct PagedLaunch {
 
 // Byte offsets of the workspace.  (A call whose rows all together are no more
 // than few_rows() has no segment for the kernel for many rows.)
+struct PagedSection {
+  size_t at, bytes;
+};
 struct PagedWorkspace {
-  size_t few_o, few_ml, few_join, chunk_o, chunk_ml, chunk_join, bytes;
+  PagedSection few_o, few_ml, few_join, chunk_o, chunk_ml, chunk_join;
+  size_t bytes;
   int32_t few_rows;
 };
 inline PagedWorkspace paged_workspace(int64_t total_rows, int32_t head_dim) {  // of either type
   size_t at = 0;
   auto take = [&at](size_t bytes) {
-    const size_t a = at;
+    const PagedSection a{at, bytes};
     at += (bytes + 255) & ~size_t(255);
     return a;
   };

@@ -208,7 +208,6 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   unsigned int* err = nullptr;
   if ((st = launch_device(&sms, &err)) != VARLEN_OK) return st;
   if (total_q == 0) return VARLEN_OK;
-  const int64_t es = elem_bytes(c);
   PagedLaunch L;
   std::memset(&L, 0, sizeof(L));
   PagedParams& p = L.p;
@@ -219,21 +218,10 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   p.o_rs = so.row;
   p.o_hs = so.head;
   p.lse = lse;
-  p.k = static_cast<const uint8_t*>(c.k);
-  p.v = static_cast<const uint8_t*>(c.v);
-  p.k_page = c.sk.page * es;
-  p.k_row = c.sk.row * es;
-  p.k_head = c.sk.head * es;
-  p.v_page = c.sv.page * es;
-  p.v_row = c.sv.row * es;
-  p.v_head = c.sv.head * es;
-  p.k_scale = static_cast<const __nv_bfloat16*>(c.k_scale);
-  p.v_scale = static_cast<const __nv_bfloat16*>(c.v_scale);
   p.pages = view_of(c, shift);
   p.cu_q = cu_seqlens_q;
   p.batch = batch;
   p.total_q = total_q;
-  p.num_heads = num_heads;
   p.kv_heads = c.num_kv_heads;
   p.group = num_heads / c.num_kv_heads;
   p.few_rows = few_rows(c.type == VARLEN_CACHE_E4M3);
@@ -245,10 +233,6 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   p.q_span = nhd_bytes(q, sq, total_q, num_heads, c.head_dim);
   p.out_span = nhd_bytes(out, so, total_q, num_heads, c.head_dim);
   p.lse_span = checked_span(lse, (int64_t)num_heads * total_q * 4);
-  p.kp_span = checked_span(c.k, pages_bytes(c, c.sk));
-  p.vp_span = checked_span(c.v, pages_bytes(c, c.sv));
-  p.ks_span = checked_span(c.k_scale, scale_bytes(c));
-  p.vs_span = checked_span(c.v_scale, scale_bytes(c));
   L.head_dim = c.head_dim;
   L.sms = std::min(sms, kMaxSms);
   L.e4m3 = c.type == VARLEN_CACHE_E4M3;
@@ -267,10 +251,13 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   if (L.many && tiles <= (int64_t)(L.e4m3 ? 24 : 64) * sms) L.few = false;
   char* ws = static_cast<char*>(workspace);
   const PagedWorkspace w = paged_workspace(total_rows, c.head_dim);
-  L.few_parts = PagedParts{reinterpret_cast<float*>(ws + w.few_o), reinterpret_cast<float*>(ws + w.few_ml),
-                           reinterpret_cast<PagedJoin*>(ws + w.few_join), w.few_rows};
-  L.chunk = PagedParts{reinterpret_cast<float*>(ws + w.chunk_o), reinterpret_cast<float*>(ws + w.chunk_ml),
-                       reinterpret_cast<PagedJoin*>(ws + w.chunk_join), kChunkRows};
+  auto parts = [ws](PagedSection o, PagedSection ml, PagedSection join, int32_t rows) {
+    auto span = [ws](PagedSection s) { return checked_span(ws + s.at, (int64_t)s.bytes); };
+    return PagedParts{reinterpret_cast<float*>(ws + o.at), reinterpret_cast<float*>(ws + ml.at),
+                      reinterpret_cast<PagedJoin*>(ws + join.at), rows, span(o), span(ml), span(join)};
+  };
+  L.few_parts = parts(w.few_o, w.few_ml, w.few_join, w.few_rows);
+  L.chunk = parts(w.chunk_o, w.chunk_ml, w.chunk_join, kChunkRows);
   auto maps = [&](CUtensorMap* k, CUtensorMap* v, CUtensorMap* ks, CUtensorMap* vs, int tile) {
     const int box = std::min(c.page_size, tile);
     int s2;

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       if (lane == 0) {
-        parts.join[2 * blockIdx.x].parts = parts.join[2 * blockIdx.x + 1].parts = 0;
+        clear_join(p, parts);
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         }
         __syncwarp();
         if (lane == 0) {
-          if (more) paged_note(parts.join, sh.start, x);
+          if (more) paged_note(p, parts, sh.start, x);
           sh.piece[slot] = x;
           mbar_arrive(&sh.piece_full[slot]);
         }
@@ -490,7 +490,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         } else if (live) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(part + d0 + 4 * i) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            if (in_span(parts.o_span, part + d0 + 4 * i, 16, p.err))
+              *reinterpret_cast<uint4*>(part + d0 + 4 * i) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
       if (live && whole) {
@@ -499,7 +500,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
           *la = l == 0.f ? -INFINITY : (m_use + __log2f(l)) * 0.69314718055994531f;
       } else if (live) {
         const int64_t r = (2 * (int64_t)blockIdx.x + (x.begins() ? 1 : 0)) * parts.rows + hf * 128 + row;
-        *reinterpret_cast<float2*>(parts.ml + 2 * r) = make_float2(m_use, l);
+        if (in_span(parts.ml_span, parts.ml + 2 * r, 8, p.err))
+          *reinterpret_cast<float2*>(parts.ml + 2 * r) = make_float2(m_use, l);
       }
       tc_fence_before();
       g += tiles;

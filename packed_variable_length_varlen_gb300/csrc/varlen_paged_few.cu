@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
   if (warp == C::WARPS) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      parts.join[2 * blockIdx.x].parts = parts.join[2 * blockIdx.x + 1].parts = 0;
+      clear_join(p, parts);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
     bool ok = true;
     walk.init(sh.start, p, take);
     while (ok && walk.next(p, x)) {
-      if (lane == 0) paged_note(parts.join, sh.start, x);
+      if (lane == 0) paged_note(p, parts, sh.start, x);
       const int32_t tiles = min(x.j1, x.u.tiles);
       for (int32_t j = x.j0; ok && j < tiles; ++j) {
         const int32_t key = (x.u.tile0 + j) * C::KT + (piece << box_shift);
@@ -669,16 +669,22 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
           float* oa = parts.o + row * D;
           if constexpr (E4M3) {
 #pragma unroll
-            for (int t = 0; t < C::MT; t += 2)
-              *reinterpret_cast<float4*>(oa + r * (D / 8) + 2 * t) =
-                  make_float4(o[t][i], o[t][2 + i], o[t + 1][i], o[t + 1][2 + i]);
+            for (int t = 0; t < C::MT; t += 2) {
+              float* d = oa + r * (D / 8) + 2 * t;
+              if (in_span(parts.o_span, d, 16, p.err))
+                *reinterpret_cast<float4*>(d) = make_float4(o[t][i], o[t][2 + i], o[t + 1][i], o[t + 1][2 + i]);
+            }
           } else {
 #pragma unroll
             for (int t = 0; t < C::MT; ++t)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) oa[t * 16 + e * 8 + r] = o[t][2 * e + i];
+              for (int e = 0; e < 2; ++e) {
+                float* d = oa + t * 16 + e * 8 + r;
+                if (in_span(parts.o_span, d, 4, p.err)) *d = o[t][2 * e + i];
+              }
           }
-          if (r == 0) *reinterpret_cast<float2*>(parts.ml + row * 2) = make_float2(m[i], l[i]);
+          float* ml = parts.ml + row * 2;
+          if (r == 0 && in_span(parts.ml_span, ml, 8, p.err)) *reinterpret_cast<float2*>(ml) = make_float2(m[i], l[i]);
         }
       }
     }

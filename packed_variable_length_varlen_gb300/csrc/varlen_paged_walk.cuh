@@ -263,26 +263,40 @@ struct PagedWalk {
   }
 };
 
+// Entry i of the join's list.
+__device__ __forceinline__ void put_join(const PagedParams& p, const PagedParts& parts, int32_t i, const PagedJoin& u) {
+  if (in_span(parts.join_span, parts.join + i, sizeof(PagedJoin), p.err)) parts.join[i] = u;
+}
+__device__ __forceinline__ PagedJoin get_join(const PagedParams& p, const PagedParts& parts, int32_t i) {
+  return in_span(parts.join_span, parts.join + i, sizeof(PagedJoin), p.err) ? parts.join[i] : PagedJoin{0, 0, 0, 0, 0};
+}
+// This CTA's entries, empty: no unit that the join would have to look at.
+__device__ __forceinline__ void clear_join(const PagedParams& p, const PagedParts& parts) {
+  put_join(p, parts, 2 * blockIdx.x, PagedJoin{0, 0, 0, 0, 0});
+  put_join(p, parts, 2 * blockIdx.x + 1, PagedJoin{0, 0, 0, 0, 0});
+}
+
 // A CTA that cannot work: an error, and no unit for the join (which would take
 // what the workspace happens to hold for one).
 __device__ __forceinline__ void paged_refuse(const PagedParams& p, const PagedParts& parts) {
   dependency_wait();
   if (threadIdx.x != 0) return;
-  parts.join[2 * blockIdx.x].parts = parts.join[2 * blockIdx.x + 1].parts = 0;
+  clear_join(p, parts);
   record_error(p.err, kErrBounds);
 }
 
 // Left for the join by the one thread that calls it, for every piece: the
 // units that the CTA holds a part of (its first and its last piece, if any).
-__device__ __forceinline__ void paged_note(PagedJoin* join, const PagedStart& st, const PagedPiece& x) {
+__device__ __forceinline__ void paged_note(const PagedParams& p, const PagedParts& parts, const PagedStart& st,
+                                           const PagedPiece& x) {
   if (x.whole()) return;
   // the unit's first and last tile in the launch's list (x is the CTA's last
   // piece where it begins the unit, its first where it does not)
   const int64_t begin = x.begins() ? st.first + st.count - x.j1 : st.first - x.j0;
   const PagedShares shares(st.total, st.ctas);
   const int32_t first = shares.owner(begin);
-  join[2 * blockIdx.x + (x.begins() ? 1 : 0)] =
-      PagedJoin{x.b, x.kh, x.blk, first, shares.owner(begin + x.cost - 1) - first + 1};
+  put_join(p, parts, 2 * blockIdx.x + (x.begins() ? 1 : 0),
+           PagedJoin{x.b, x.kh, x.blk, first, shares.owner(begin + x.cost - 1) - first + 1});
 }
 
 }  // namespace varlen

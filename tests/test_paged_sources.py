@@ -53,7 +53,7 @@ def test_a_warp_parts_its_rows_in_the_join():
     body = text[text.index("void join_by_warp("):]
     body = body[:body.index("\n}\n")]
     assert body.rstrip().endswith("__syncwarp();")
-    assert body.index("weight[2 * k] = ex2") < body.index("__syncwarp();") < body.index("fmaf(oa")
+    assert body.index("weight[2 * k] = ex2") < body.index("__syncwarp();") < body.index("o[i] = fmaf(")
 
 
 def test_a_kernel_that_returns_early_leaves_the_join_nothing():
@@ -65,7 +65,7 @@ def test_a_kernel_that_returns_early_leaves_the_join_nothing():
     walk = _source("varlen_paged_walk.cuh")
     body = walk[walk.index("void paged_refuse("):]
     body = body[:body.index("\n}\n")]
-    assert body.index("dependency_wait();") < body.index("parts = 0;") < body.index("record_error")
+    assert body.index("dependency_wait();") < body.index("clear_join(p, parts);") < body.index("record_error")
 
 
 def test_a_wait_that_can_give_up_has_one_outcome_for_a_warp():

@@ -1,6 +1,10 @@
-"""The paged attention's ways through its kernels, on a GPU: units of every
-number of rows that several CTAs share, so that the joins take each of their
-forms, against the plain 64-bit form."""
+"""The paged attention's ways through its kernels, on a GPU, against the plain
+64-bit form: units of every number of rows that several CTAs share, so that the
+joins take each of their forms; hints that choose the kernel for few rows at
+every group size; and each call with tables that make one kernel take all of
+it and with tables wide enough that both run."""
+import random
+
 import pytest
 import torch
 
@@ -52,6 +56,12 @@ def _check(va, new, lens, heads, kv, dim, page, kind, hint, columns=1, sizes=Non
     _ok(va)
 
 
+def _wide(batch, kv, page):
+    """Table columns with which a call of several segments is taken for long whatever its lengths are: 256 tiles of
+    128 keys for each of 160 SMs."""
+    return -(-256 * 160 * 128 // (batch * kv * page))
+
+
 # A CTA takes at least two tiles of 64 keys: 300 keys are 3 parts of a unit, 1900 are 15, 2100 are 17, 9000 are 71.
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("dim", [64, 96, 128])
@@ -61,3 +71,68 @@ def test_units_of_few_rows_in_parts(va, kind, dim, tokens, group, keys):
     """One sequence, two key heads; up to 16 rows (bf16) or 32 (E4M3) a unit, in parts that warps join (up to 16) and
     that blocks do.  (bf16 units of more rows go to the kernel for many, whose join takes a row a warp.)"""
     _check(va, [tokens], [keys], 2 * group, 2, dim, 64, kind, tokens, sizes=[0.05, 1.0, 6.0], repeats=6)
+
+
+LENS = [5, 7, 0, 200, 64, 16, 700, 3, 129, 65, 2100]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("group,kv,page", [(1, 2, 16), (3, 2, 128), (4, 1, 64), (7, 2, 32), (8, 1, 16), (16, 1, 256)])
+@pytest.mark.parametrize("window", [(-1, -1), (37, -1)])
+def test_the_kernel_for_few_rows_at_every_group(va, kind, dim, group, kv, page, window):
+    """Segments of up to 16 (bf16) or 32 (E4M3) rows with the hint that says so: no other kernel takes part."""
+    most = max((32 if kind == "e4m3" else 16) // group, 1)
+    r = random.Random(group)
+    new = [most, 0, 1] + [r.randint(0, most) for _ in LENS[3:]]
+    _check(va, new, LENS, group * kv, kv, dim, page, kind, most, window=window)
+
+
+NEW = [130, 1, 0, 257, 4, 65, 33, 2, 1, 1, 3]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("group,kv,page", [(1, 2, 16), (4, 2, 64), (7, 1, 32), (3, 1, 1024), (8, 2, 128), (20, 1, 64)])
+@pytest.mark.parametrize("hint", [0, 257])
+@pytest.mark.parametrize("wide", [False, True])
+def test_chunks_beside_tokens_both_ways(va, kind, dim, group, kv, page, hint, wide):
+    _check(va, NEW, LENS, group * kv, kv, dim, page, kind, hint, columns=_wide(len(NEW), kv, page) if wide else 1,
+           repeats=2)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hint", [0, 1, 2, 1000000])
+@pytest.mark.parametrize("wide", [False, True])
+def test_hints_both_ways(va, kind, hint, wide):
+    _check(va, [1, 200, 7], [300, 800, 64], 4, 2, 128, 64, kind, hint, columns=_wide(3, 2, 64) if wide else 1)
+
+
+@pytest.mark.parametrize("seed", range(16))
+@pytest.mark.parametrize("wide", [False, True])
+def test_drawn_shapes_both_ways(va, seed, wide):
+    r = random.Random(100 + seed)
+    kv, group, batch = r.choice((1, 2, 3, 8)), r.choice((1, 2, 3, 5, 7, 8, 12, 16, 33)), r.choice((2, 5, 40))
+    page, most = r.choice((16, 32, 64, 128, 256, 512, 1024)), r.choice((4, 30, 250))
+    new = [r.choice((1, 1, r.randint(0, most))) for _ in range(batch)]
+    lens = [r.randint(0, r.choice((20, 300, 2500))) for _ in range(batch)]
+    _check(va, new, lens, kv * group, kv, r.choice((64, 96, 128)), page, r.choice(("bf16", "e4m3")), r.choice((0, max(new))),
+           columns=_wide(batch, kv, page) if wide else 1, window=(r.choice((-1, -1, 0, 5, 100, 1000)), -1), seed=seed)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_both_kernels_on_several_streams(va, kind):
+    """Calls of both kernels, several at once, each with its own workspace: the bits of a call alone."""
+    new, lens = [40, 1, 3], [5000, 3000, 700]
+    cache, _, _ = C.make_cache(lens, 2, 128, 64, kind, DEV, columns=_wide(3, 2, 64))
+    cu = C.cu_of(new, DEV)
+    qs = [_rows(sum(new), 8, 128, s) for s in (1, 2, 3)]
+    alone = [va.attention_fwd_paged(q, cache, cu, causal=True) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(8):
+        got = [va.attention_fwd_paged(q, cache, cu, causal=True, stream=s) for q, s in zip(qs, streams)]
+        torch.cuda.synchronize()
+        for (o, l), (o1, l1) in zip(alone, got):
+            assert torch.equal(o, o1) and torch.equal(l, l1)
+    _ok(va)

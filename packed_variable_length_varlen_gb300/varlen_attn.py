@@ -768,8 +768,8 @@ def attention_fwd_paged(q, cache, cu_seqlens_q, max_seqlen_q=0, scale=None, out=
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
         fresh.append(workspace)
     else:
-        if workspace.device != cache.device:
-            raise ValueError("the workspace must be on the cache's device")
+        if workspace.device != cache.device or not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous and on the cache's device")
         nbytes = workspace.numel() * workspace.element_size()
     left, right = _band(causal, window) or (-1, -1)
     _paged_call(LIB.varlen_attn_fwd_paged, cache, stream, fresh,

@@ -223,3 +223,15 @@ def test_the_handle_refuses_other_tensors(va, kind):
     c.block_table[0, 1] = 5
     assert t["seqlens"].tolist() == [3, 3, 3] and int(t["block_table"][0, 1]) == 5
     assert c.struct.seqlens == t["seqlens"].data_ptr()
+
+
+def test_the_binding_refuses_a_workspace_with_gaps(va):
+    """The kernels use the workspace's bytes one after another: an expanded or strided tensor does not have as many as
+    its element count says."""
+    c = va.PagedCache(**_tensors())
+    cu = torch.tensor([0, 1, 2, 4], dtype=torch.int32)
+    q = torch.zeros(4, 4, 64, dtype=torch.bfloat16)
+    need = va.varlen_attn_fwd_paged_workspace_size(3, 4, 4, 2, 64)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(need), torch.zeros(2 * need, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            va.attention_fwd_paged(q, c, cu, workspace=ws)

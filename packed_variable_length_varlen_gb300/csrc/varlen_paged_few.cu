@@ -378,15 +378,15 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
                 mma16816<false>(s2, u[i].z, v[i].z, u[i].w, v[i].w, qf[2 * i + 1][0], qf[2 * i + 1][1]);
               }
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] = (s[e] + s2[e]) * rowf[e & 1];
             if constexpr (E4M3) {
+              // the row's and the key's factor first: either alone may take the sum out of range
               const float k0 = __bfloat162float(lds<__nv_bfloat16>(ksc + scale_at(a + r, box_shift)));
               const float k1 = __bfloat162float(lds<__nv_bfloat16>(ksc + scale_at(a + r + 8, box_shift)));
-              s[0] *= k0;
-              s[1] *= k0;
-              s[2] *= k1;
-              s[3] *= k1;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[e] = (s[e] + s2[e]) * (rowf[e & 1] * (e < 2 ? k0 : k1));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[e] = (s[e] + s2[e]) * rowf[e & 1];
             }
           }
           if (a + share * C::STEP >= C::KT) {  // the warp's last step on this K tile

@@ -79,3 +79,32 @@ def test_values_that_grow(va, kind, tokens, heads, gap):
         v *= torch.exp2(torch.linspace(-15, 15, KEYS, device=DEV))[:, None, None]
 
     _call(va, kind, tokens, heads, gap, value)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 9, 100])
+@pytest.mark.parametrize("shift", [-122, -116, -104, 104, 116, 122])
+def test_queries_and_keys_at_opposite_ends_of_the_range(va, kind, n, shift):
+    """Queries times 2^shift and keys times 2^-shift: the same scores.  Up to 2^104 the same bits as well, as every
+    number keeps its own: the least are near 2^-20, and bf16 is normal down to 2^-126.  Beyond, the smaller side
+    holds subnormal numbers, which are not those of the unshifted call any more: the check is the plain form's on the
+    numbers that there are."""
+    ln, dim, heads = 200, 128, 2
+    g = torch.Generator().manual_seed(5)
+    k, v = (torch.randn(ln, heads, dim, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    q, cu = torch.randn(n, 4, dim, generator=g).to(torch.bfloat16).to(DEV), C.cu_of([n], DEV)
+    got = []
+    for e in (0, shift):
+        cache, _, _ = C.make_cache([ln], heads, dim, 32, kind, DEV)
+        ke, qe = (k.double() * 2.0 ** -e).to(torch.bfloat16), (q.double() * 2.0 ** e).to(torch.bfloat16)
+        va.cache_write(cache, ke, v, C.cu_of([ln], DEV))
+        got.append(va.attention_fwd_paged(qe, cache, cu, max_seqlen_q=n, causal=True))
+        assert va.varlen_attn_get_device_status() == 0
+        kh, vh = ke.double(), v.double()
+        if kind == "e4m3":
+            (kc, ks), (vc, vs) = C.quantise(ke), C.quantise(v)
+            kh, vh = kc.double() * ks.double()[..., None], vc.double() * vs.double()[..., None]
+        ref = C.attend(qe, kh, vh, float(torch.tensor(dim ** -0.5, dtype=torch.float32)), -1, 0)
+        C.check_attend(got[-1][0], got[-1][1], ref, dim, ln)
+    if abs(shift) <= 104:
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])

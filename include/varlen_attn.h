@@ -407,7 +407,7 @@ int varlen_attn_cache_read(const varlen_kv_cache* cache, const int32_t* cu_seqle
  *
  * max_seqlen_q chooses kernels only and is never trusted for correctness:
  * when it is positive and max_seqlen_q * num_heads / num_kv_heads is at most
- * 16 (bf16) or 32 (E4M3), the kernel for few rows takes every segment;
+ * 16, the kernel for few rows takes every segment;
  * otherwise each segment is taken by the kernel that its own length calls for,
  * or, where that costs more launches than it gives, all by the one for many.
  *

@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     const PagedJoin u = units[which];
     if (u.parts == 0 || (which == 0 && u.parts <= kWarpParts)) continue;  // block-uniform
     const int32_t q0 = clamp_row(p.cu_q[u.b], p.total_q), q1 = clamp_row(p.cu_q[u.b + 1], p.total_q);
-    const int32_t first = u.blk * p.few_rows, rows = min((q1 - q0) * p.group - first, p.few_rows);
+    const int32_t first = u.blk * kFewRows, rows = min((q1 - q0) * p.group - first, kFewRows);
     auto row_of = [&](int32_t row) {
       const int32_t tok = (first + row) / p.group;
       return JoinRow{(int64_t)q0 + tok, u.kh * p.group + first + row - tok * p.group};

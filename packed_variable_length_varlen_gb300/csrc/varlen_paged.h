@@ -99,7 +99,6 @@ struct PagedParams {
   PageView pages;  // (keys, values and scales are read by TMA alone)
   const int32_t* cu_q;
   int32_t batch, total_q, kv_heads, group;
-  int32_t few_rows;  // up to which the kernel for few rows takes a segment
   int64_t win_left, win_right;
   float scale_log2;
   unsigned int* err;
@@ -107,15 +106,18 @@ struct PagedParams {
   Span q_span, out_span, lse_span;  // bounds-checking build
 };
 
-// What a kernel takes: segments of at most few_rows() rows, of more, or all.
+// What a kernel takes: segments of at most kFewRows rows, of more, or all.
 enum PagedTake : int32_t { kTakeFew = 0, kTakeMany = 1, kTakeAll = 2 };
 
 // Rows (queries x heads of a group) up to which the kernel for few rows takes a
-// segment, and rows of its units.  64 sequences of up to 8192 keys, 8 key heads
-// of 128, us for the kernel for few rows and the one for many: bf16 16 rows 174
-// and 212, 32 rows 250 and 212; E4M3 16 rows 170 and 269, 32 rows 287 and 270.
-constexpr int few_rows(bool e4m3) { return e4m3 ? 32 : 16; }
-constexpr int kMostFewRows = 32;
+// segment, and rows of its units.  us for the kernel for few rows and the one for
+// many, one token a sequence, D = 128, 64 ragged sequences of up to 8192 keys
+// and 8 key heads / 64 of 1000 and 8 / 32 of 8000 and 2 / 4 of 4000 and 8 / one
+// of 60000 and 2: at 16 rows E4M3 166 and 220 / 52 and 82 / 50 and 61; at 17
+// E4M3 272 and 225 / 80 and 89 / 78 and 64 / 38 and 29 / 34 and 37, bf16 315 and
+// 192 / 94 and 72 / 90 and 59 / 27 and 26 / 27 and 36; from there to 32 rows
+// neither changes by more than a tenth.
+constexpr int kFewRows = 16;
 constexpr int kFewTile = 64;      // keys per tile of that kernel
 // its CTAs on an SM: E4M3 rows are half as long, so more of them have to be in the making
 constexpr int few_ctas(bool e4m3) { return e4m3 ? 3 : 2; }
@@ -153,7 +155,7 @@ struct PagedLaunch {
 };
 
 // Byte offsets of the workspace.  (A call whose rows all together are no more
-// than few_rows() has no segment for the kernel for many rows.)
+// than kFewRows has no segment for the kernel for many rows.)
 struct PagedSection {
   size_t at, bytes;
 };
@@ -170,8 +172,8 @@ inline PagedWorkspace paged_workspace(int64_t total_rows, int32_t head_dim) {  /
     return a;
   };
   PagedWorkspace w;
-  w.few_rows = (int32_t)(total_rows < kMostFewRows ? (total_rows < 1 ? 1 : total_rows) : kMostFewRows);
-  const size_t few = (size_t)few_ctas(true) * kMaxSms, many = total_rows > few_rows(false) ? kMaxSms : 0;
+  w.few_rows = (int32_t)(total_rows < kFewRows ? (total_rows < 1 ? 1 : total_rows) : kFewRows);
+  const size_t few = (size_t)few_ctas(true) * kMaxSms, many = total_rows > kFewRows ? kMaxSms : 0;
   w.few_o = take(2 * few * w.few_rows * head_dim * 4);
   w.few_ml = take(2 * few * w.few_rows * 8);
   w.few_join = take(2 * few * sizeof(PagedJoin));

@@ -224,7 +224,6 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   p.total_q = total_q;
   p.kv_heads = c.num_kv_heads;
   p.group = num_heads / c.num_kv_heads;
-  p.few_rows = few_rows(c.type == VARLEN_CACHE_E4M3);
   p.win_left = window_left < 0 ? kWinUnbounded : window_left;
   p.win_right = window_right < 0 ? kWinUnbounded : window_right;
   p.scale_log2 = scale * kLog2e;
@@ -245,8 +244,9 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   // 16 x 2000 keys (13 tiles an SM) 45 and 35, 16 x 8192 (51) 85 and 80, 64 x
   // 8192 (216) 212 and 257; E4M3 13 tiles 45 and 41, 26 57 and 55, 51 78 and 84.
   const int64_t total_rows = (int64_t)total_q * p.group;
-  L.few = total_rows <= p.few_rows || batch > 1 || (max_seqlen_q > 0 && (int64_t)max_seqlen_q * p.group <= p.few_rows);
-  L.many = total_rows > p.few_rows && !(max_seqlen_q > 0 && (int64_t)max_seqlen_q * p.group <= p.few_rows);
+  const bool known_few = total_rows <= kFewRows || (max_seqlen_q > 0 && (int64_t)max_seqlen_q * p.group <= kFewRows);
+  L.few = known_few || batch > 1;
+  L.many = !known_few;  // (so total_rows > kFewRows, and the workspace has its sections)
   const int64_t tiles = (int64_t)batch * c.num_kv_heads * ((((int64_t)c.max_pages << shift) + kChunkTile - 1) / kChunkTile);
   if (L.many && tiles <= (int64_t)(L.e4m3 ? 24 : 64) * sms) L.few = false;
   char* ws = static_cast<char*>(workspace);

@@ -1,15 +1,14 @@
 // varlen_paged_few.cu -- attention over the paged cache for few query rows:
 // single tokens, drafted tokens, short chunks.
 //
-// Bound: every key and value is read once for at most 16 (bf16) or 32 (E4M3)
-// rows (query tokens times the query heads that share a key head), so the
-// memory's rate decides and the matrix products only have to keep up with it.  At 6.8 TB/s an SM
-// receives 44.7 bytes a nanosecond, 12 bf16 or 23 E4M3 elements a cycle.  The
-// warp-level m16n8k16 products take keys (then columns of V) as their 16 rows
-// and query rows as their 8 columns, S^T = K Q^T and O^T = V^T P^T: a step of 16
-// keys for 8 rows is 16 products at D = 128, and o takes 32 registers, so that
-// enough warps stay resident to hide the chain of products, softmax and
-// products.  (The other way round, 16 query rows by 8 keys, costs twice the
+// Bound: every key and value is read once for at most 16 rows (query tokens
+// times the query heads that share a key head), so the memory's rate decides and
+// the matrix products only have to keep up with it.  At 6.8 TB/s an SM receives
+// 44.7 bytes a nanosecond, 12 bf16 or 23 E4M3 elements a cycle.  The warp-level
+// m16n8k16 products take keys (then columns of V) as their 16 rows and query
+// rows as their 8 columns, S^T = K Q^T and O^T = V^T P^T: a step of 16 keys for 8
+// rows is 16 products at D = 128, and o takes 32 registers, so that enough warps
+// stay resident to hide the chain of products, softmax and products.  (The other way round, 16 query rows by 8 keys, costs twice the
 // products and registers while most of the 16 rows are empty: 214 us where this
 // form took 190 for 64 ragged E4M3 sequences, and 124 with the third CTA an SM that
 // its registers leave room for.)  Measured: 8 sequences of 17580 bf16 keys, 56
@@ -71,7 +70,7 @@ struct FewCfg {
   static constexpr int THREADS = (WARPS + 1) * 32;
   static constexpr int KT = kFewTile;                       // keys per tile
   static constexpr int STEP = 16;                           // keys a warp takes at a time
-  static constexpr int ROWS = few_rows(E4M3);
+  static constexpr int ROWS = kFewRows;
   using Geom = PagedGeom<ROWS, KT, false>;
   static constexpr int CK = E4M3 ? 1 : (D + 63) / 64;       // 128-byte column chunks of a row
   static constexpr int CHUNK = KT * 128;
@@ -264,7 +263,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
       // rows of the unit: first is row `skip` of token t0
       const int32_t skip = x.blk * C::ROWS - x.u.t0 * p.group;
       const int32_t rows = min((x.n - x.u.t0) * p.group - skip, C::ROWS);
-      const int mt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);  // row tiles
+      const int mt = rows <= 8 ? 1 : 2;  // row tiles
       const int rt = warp & (mt - 1), kg = warp / mt, share = C::WARPS / mt;
       const bool works = rt * 8 < rows;
       // the operand B holds row r of the tile; the sums hold rows 2c, 2c + 1

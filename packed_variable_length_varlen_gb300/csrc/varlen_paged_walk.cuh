@@ -71,7 +71,7 @@ __device__ __forceinline__ PagedSeg paged_seg(const PagedParams& p, int32_t b, i
   s.q0 = a;
   s.n = max(e - a, 0);
   s.sk = cache_len(p.pages, b);
-  const bool few = s.n * p.group <= p.few_rows;  // (total_q * num_heads < 2^31)
+  const bool few = s.n * p.group <= kFewRows;  // (total_q * num_heads < 2^31)
   if ((take == kTakeFew && !few) || (take == kTakeMany && few)) s.n = 0;
   s.blocks = G::blocks(p, s.n);
   s.per_head = 0;

@@ -68,8 +68,8 @@ def _wide(batch, kv, page):
 @pytest.mark.parametrize("tokens,group", [(1, 16), (2, 8), (5, 3), (17, 1), (6, 3), (3, 7), (4, 6), (3, 9), (4, 8), (1, 31)])
 @pytest.mark.parametrize("keys", [300, 1900, 2100, 9000])
 def test_units_of_few_rows_in_parts(va, kind, dim, tokens, group, keys):
-    """One sequence, two key heads; up to 16 rows (bf16) or 32 (E4M3) a unit, in parts that warps join (up to 16) and
-    that blocks do.  (bf16 units of more rows go to the kernel for many, whose join takes a row a warp.)"""
+    """One sequence, two key heads; up to 16 rows a unit, in parts that warps join (up to 16) and that blocks do, and
+    up to 32, which the kernel for many rows takes (its join takes a row a warp)."""
     _check(va, [tokens], [keys], 2 * group, 2, dim, 64, kind, tokens, sizes=[0.05, 1.0, 6.0], repeats=6)
 
 
@@ -81,8 +81,8 @@ LENS = [5, 7, 0, 200, 64, 16, 700, 3, 129, 65, 2100]
 @pytest.mark.parametrize("group,kv,page", [(1, 2, 16), (3, 2, 128), (4, 1, 64), (7, 2, 32), (8, 1, 16), (16, 1, 256)])
 @pytest.mark.parametrize("window", [(-1, -1), (37, -1)])
 def test_the_kernel_for_few_rows_at_every_group(va, kind, dim, group, kv, page, window):
-    """Segments of up to 16 (bf16) or 32 (E4M3) rows with the hint that says so: no other kernel takes part."""
-    most = max((32 if kind == "e4m3" else 16) // group, 1)
+    """Segments of up to 16 rows with the hint that says so: no other kernel takes part."""
+    most = 16 // group
     r = random.Random(group)
     new = [most, 0, 1] + [r.randint(0, most) for _ in LENS[3:]]
     _check(va, new, LENS, group * kv, kv, dim, page, kind, most, window=window)

@@ -239,16 +239,19 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   // alone; a single segment of more rows goes to the other one whatever its
   // length.  Of the rest, calls whose tables can name few key tiles go to the
   // one for many rows alone, which is two launches less; otherwise both run
-  // and each takes the segments that are its own.  Measured with 13 single
-  // tokens and 3 chunks of 10..60 tokens, 32/8 heads, us both and one: bf16
-  // 16 x 2000 keys (13 tiles an SM) 45 and 35, 16 x 8192 (51) 85 and 80, 64 x
-  // 8192 (216) 212 and 257; E4M3 13 tiles 45 and 41, 26 57 and 55, 51 78 and 84.
+  // and each takes the segments that are its own.  Measured with 13 (29, 61)
+  // single tokens and 3 chunks of 10..60 tokens, 32/8 heads, us both and one, for
+  // sequences of full and of ragged length: E4M3 16 x 4000 keys (27 tiles an SM)
+  // 84 and 83 / 78 and 64, 16 x 6000 (40) 97 and 106 / 77 and 67, 16 x 8192 (54)
+  // 115 and 135 / 77 and 88, 64 x 8192 (216) 237 and 463 / 179 and 233; bf16 16 x
+  // 8192 132 and 125 / 85 and 77, 32 x 8192 (108) 206 and 224 / 121 and 110, 64 x
+  // 8192 353 and 422 / 201 and 203.
   const int64_t total_rows = (int64_t)total_q * p.group;
   const bool known_few = total_rows <= kFewRows || (max_seqlen_q > 0 && (int64_t)max_seqlen_q * p.group <= kFewRows);
   L.few = known_few || batch > 1;
   L.many = !known_few;  // (so total_rows > kFewRows, and the workspace has its sections)
   const int64_t tiles = (int64_t)batch * c.num_kv_heads * ((((int64_t)c.max_pages << shift) + kChunkTile - 1) / kChunkTile);
-  if (L.many && tiles <= (int64_t)(L.e4m3 ? 24 : 64) * sms) L.few = false;
+  if (L.many && tiles <= (int64_t)(L.e4m3 ? 40 : 64) * sms) L.few = false;
   char* ws = static_cast<char*>(workspace);
   const PagedWorkspace w = paged_workspace(total_rows, c.head_dim);
   auto parts = [ws](PagedSection o, PagedSection ml, PagedSection join, int32_t rows) {

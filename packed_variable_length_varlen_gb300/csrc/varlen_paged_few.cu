@@ -34,6 +34,12 @@
 // for the order of O's columns: with E4M3 a lane reads D/8 consecutive bytes of
 // each of its four keys, which stand for its row of D/8 different half-tiles.
 //
+// bf16: the products want P in V's type.  One bf16 of it would put 2^-9 of each
+// weight's size into O, as much again as O's own rounding, so P comes in two
+// parts of 8 bits, hi + lo, and V is multiplied by both: twice the products of
+// that half, which the memory hides (8 sequences of 17580 keys 584 us either
+// way; 4 drafted tokens of 4 sequences 15.8 and 15.9).
+//
 // E4M3 codes become f16 (exact, two a conversion) and both products run in
 // f16 with 32-bit sums.  What f16 lacks in range the scales make up for:
 //   S: a row of Q is multiplied by the power of two that brings its largest
@@ -48,7 +54,8 @@
 //      instead, so that P_j is held to bf16's 8 bits or better down to 2^-21 of
 //      the row's largest weight whatever the scales are: a code's bits s eeee mmm
 //      moved to s 0000eeee mmm0000 are the bf16 code * 2^-120, subnormals too,
-//      times 2^127 s / R, and P times 2^6.  A vector of zeros has a scale of 1
+//      times 2^127 s / R, and P times 2^6 (one bf16 of P: there are no registers
+//      left for a second).  A vector of zeros has a scale of 1
 //      that says nothing of its neighbours' size: it counts as one that is not
 //      there, and R does not follow it.
 #include <cuda_fp8.h>
@@ -565,12 +572,17 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
             }
           } else {
             const uint32_t row = a + (lane & 15);
-            const uint32_t p0 = transpose8(pack_bf16x2(s[0], s[1])), p1 = transpose8(pack_bf16x2(s[2], s[3]));
+            // P in two bf16 parts, the second what the first leaves: 16 bits of it
+            const uint32_t h0 = pack_bf16x2(s[0], s[1]), h1 = pack_bf16x2(s[2], s[3]);
+            const uint32_t p0 = transpose8(h0), p1 = transpose8(h1);
+            const uint32_t e0 = transpose8(pack_bf16x2(s[0] - bf16_lo(h0), s[1] - bf16_hi(h0)));
+            const uint32_t e1 = transpose8(pack_bf16x2(s[2] - bf16_lo(h1), s[3] - bf16_hi(h1)));
 #pragma unroll
             for (int t = 0; t < C::MT; ++t) {
               uint32_t b[4];
               ldsm_x4_t(b, smem_addr(vt) + (t >> 2) * C::CHUNK + swz(row, ((2 * t & 7) + (lane >> 4)) * 16));
               mma16816<false>(o[t], b[0] & keep0, b[2] & keep0, b[1] & keep1, b[3] & keep1, p0, p1);
+              mma16816<false>(o[t], b[0] & keep0, b[2] & keep0, b[1] & keep1, b[3] & keep1, e0, e1);
             }
           }
         }

@@ -108,3 +108,28 @@ def test_queries_and_keys_at_opposite_ends_of_the_range(va, kind, n, shift):
         C.check_attend(got[-1][0], got[-1][1], ref, dim, ln)
     if abs(shift) <= 104:
         assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("tokens,heads", [(1, 1), (1, 8), (2, 8), (5, 3)])  # at most 16 rows
+def test_few_rows_add_nothing_to_the_outputs_own_rounding(va, kind, tokens, heads):
+    """Units of few rows: half a step of bf16 for the output (2^-8 of it), and of the sum of its terms' sizes 2^-16 for
+    weights in two bf16 parts (bf16 cache; each part's rounding at most 2^-8 of what it rounds) or 2^-11 for weights in
+    f16 (E4M3), beside the scores' errors (fp32 sums of DIM products, exp2).  All keys but the first have one weight, at
+    sixteen places between two powers of two, so that its rounding does not average out."""
+    c = 8.0 * DIM ** -0.5 / 0.6931471805599453
+    g = torch.Generator().manual_seed(3)
+    v = (torch.rand(300, 1, DIM, generator=g) + 0.5).to(torch.bfloat16).to(DEV)
+    q = torch.zeros(tokens, heads, DIM, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 8.0
+    for i in range(16):
+        k = torch.zeros(300, 1, DIM, device=DEV)
+        k[0, 0, 0] = (1 + i / 16) / c
+        cache, kk, vv = C.make_cache([300], 1, DIM, 64, kind, DEV, fill=lambda x, b, n: k.to(torch.bfloat16) if n == 0 else v)
+        out, _ = va.attention_fwd_paged(q, cache, C.cu_of([tokens], DEV), max_seqlen_q=tokens)
+        assert va.varlen_attn_get_device_status() == 0
+        o, _, A, S = C.attend(q, kk[0], vv[0], float(torch.tensor(DIM ** -0.5, dtype=torch.float32)), -1, -1)
+        e = (DIM + 8) * 2.0 ** -24 * S.T[..., None] + 2.0 ** -21 + (300 / 16 + 64) * 2.0 ** -24
+        tol = 2.0 ** -8 * o.abs() + (2.0 ** (-16 if kind == "bf16" else -11) + 2 * e) * A
+        d = (out.double() - o).abs()
+        assert (d <= tol).all(), (i, float((d / tol).max()))

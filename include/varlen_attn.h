@@ -320,11 +320,12 @@ int varlen_attn_fwd_fp8_dense(const void* q, varlen_dense_stride sq, const void*
  * Position t of sequence b is row t % page_size of the page
  * block_table[b*table_stride + t / page_size]; sequence b holds seqlens[b]
  * positions.  block_table and seqlens are device int32 arrays that the host
- * never reads; device code clamps seqlens[b] into [0, max_pages * page_size]
- * and never follows an entry outside [0, num_pages): a write there is
- * dropped, a read gives zero rows, and the call records
- * VARLEN_ERR_DEVICE_BOUNDS (varlen_attn_get_device_status).  Sequences may
- * share pages that nothing writes.
+ * never reads; reading it, device code clamps seqlens[b] into
+ * [0, max_pages * page_size], and never follows an entry outside
+ * [0, num_pages): a write there, or past the table, is dropped, a read there
+ * gives zero rows, and the call records VARLEN_ERR_DEVICE_BOUNDS
+ * (varlen_attn_get_device_status).  Sequences may share pages that nothing
+ * writes.
  *
  * type VARLEN_CACHE_BF16: bf16 elements, k_scale = v_scale = NULL.
  * type VARLEN_CACHE_E4M3: one-byte E4M3 codes and a bf16 scale for every

@@ -34,12 +34,16 @@ constexpr int kCacheThreads = 256;
 constexpr int kLanes = 4;  // lanes of one (row, head)
 
 // A packed row's place: page (num_pages: none) and row in it; found is false
-// for rows outside every segment, pos < 0 for rows before the sequence.
+// for rows outside every segment, pos < 0 for rows before the sequence.  A read
+// takes a length past what the table can name for that many positions; a write
+// does not, as the clamp would move its rows onto older ones: positions past
+// the table have no page, which is recorded as an error.
 struct Place {
   bool found;
   int32_t pos, page, row;
 };
 
+template <bool WRITE>
 __device__ __forceinline__ Place place_of(const CacheParams& p, int32_t row, int32_t b) {
   Place x{false, -1, p.pages.num_pages, 0};
   // (heads of one warp may cover several rows: walk on from its first one)
@@ -47,8 +51,12 @@ __device__ __forceinline__ Place place_of(const CacheParams& p, int32_t row, int
   const int32_t lo = clamp_row(__ldg(p.cu + b), p.total), hi = clamp_row(__ldg(p.cu + b + 1), p.total);
   if (row < lo || row >= hi) return x;
   x.found = true;
-  x.pos = cache_len(p.pages, b) - (hi - row);
+  x.pos = (WRITE ? max(p.pages.seqlens[b], 0) : cache_len(p.pages, b)) - (hi - row);
   if (x.pos < 0) return x;
+  if (WRITE && (x.pos >> p.pages.page_shift) >= p.pages.max_pages) {
+    if (p.err != nullptr) atomicOr(p.err, (unsigned int)kErrBounds);
+    return x;
+  }
   x.page = page_at(p.pages, b, x.pos >> p.pages.page_shift, p.err);
   x.row = x.pos & (p.pages.page_size - 1);
   return x;
@@ -125,7 +133,7 @@ __global__ void __launch_bounds__(kCacheThreads) varlen_cache_write_kernel(const
       v[i] = in_span(p.v_span, va + i * 32, 16, p.err) ? __ldg(reinterpret_cast<const uint4*>(va + i * 32)) : make_uint4(0, 0, 0, 0);
     }
     const int32_t b = warp_find_segment(p.cu, p.batch, p.total, __shfl_sync(0xffffffffu, (int32_t)s.row, 0));
-    const Place x = place_of(p, (int32_t)s.row, b);
+    const Place x = place_of<true>(p, (int32_t)s.row, b);
     const bool store = s.live && x.found && x.page < p.pages.num_pages;
     uint8_t* kd = p.k + (int64_t)x.page * p.k_page + (int64_t)x.row * p.k_row + (int64_t)s.head * p.k_head;
     uint8_t* vd = p.v + (int64_t)x.page * p.v_page + (int64_t)x.row * p.v_row + (int64_t)s.head * p.v_head;
@@ -177,7 +185,7 @@ __global__ void __launch_bounds__(kCacheThreads) varlen_cache_read_kernel(const 
        g0 += step) {  // warp-uniform
     const Slot s = slot_of(p, g0 + ((threadIdx.x & 31) / kLanes));
     const int32_t b = warp_find_segment(p.cu, p.batch, p.total, __shfl_sync(0xffffffffu, (int32_t)s.row, 0));
-    const Place x = place_of(p, (int32_t)s.row, b);
+    const Place x = place_of<false>(p, (int32_t)s.row, b);
     if (!s.live || !x.found) continue;
     const bool held = x.page < p.pages.num_pages;
     const uint8_t* kd = p.k + (int64_t)x.page * p.k_page + (int64_t)x.row * p.k_row + (int64_t)s.head * p.k_head;

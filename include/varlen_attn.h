@@ -335,7 +335,11 @@ int varlen_attn_fwd_fp8_dense(const void* q, varlen_dense_stride sq, const void*
  * code x / s rounded to nearest even.  A vector that holds an infinity or a
  * NaN is held as NaN: scale NaN, codes 0.  A power of two costs the codes no
  * relative precision, and code * scale is exact in bf16 (where it neither
- * overflows nor falls below bf16's normal range).
+ * overflows nor falls below bf16's normal range).  A program that fills pages
+ * itself keeps to this: scales that are powers of two, and no NaN codes
+ * (0x7f, 0xff) in rows that a query sees.  The attention's kernels take such a
+ * code for NaN or for +-480 (varlen_attn_cache_read gives NaN), so a vector
+ * that is to show as NaN has to have the scale NaN.
  *
  * k, v and the scales are 16-byte aligned; the strides are non-negative
  * multiples of 16 bytes below 2^40 bytes, and the (page, row, head) vectors
@@ -416,8 +420,12 @@ int varlen_attn_cache_read(const varlen_kv_cache* cache, const int32_t* cu_seqle
  * is caller scratch of varlen_attn_fwd_paged_workspace_size() bytes, 256-byte
  * aligned, whose contents on entry do not matter (partial results of long
  * sequences that several CTAs share; calls that overlap on the GPU need one
- * each).  Results do not depend on anything but the inputs: partial results
- * are joined in a fixed order.
+ * each).  The same call gives the same bits: partial results are joined in a
+ * fixed order.  What chooses kernels and shares (max_seqlen_q, the table's
+ * width, the lengths of the other segments, the GPU's number of SMs) may
+ * change the order of sums, and with it the rounding, but nothing else: the
+ * kernel for few rows holds weights to 16 bits (bf16) or 11 (E4M3), the one
+ * for many to bf16's 8, as the packed forward does.
  */
 size_t varlen_attn_fwd_paged_workspace_size(int32_t batch, int32_t total_q, int32_t num_heads, int32_t num_kv_heads,
                                             int32_t head_dim);

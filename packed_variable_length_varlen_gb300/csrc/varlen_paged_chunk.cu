@@ -4,11 +4,14 @@
 // Bound: 4 D operations for every visible (row, key) pair on the tensor cores;
 // the keys are read from L2 by most units.  Measured at D = 128: four chunks of
 // 1500..2048 tokens (32 heads, 8 key heads) over 4096..16384 bf16 keys, causal,
-// 850-880 us, 1220-1260 TFLOP/s; 250 tokens of 56 heads over 77000 E4M3 keys 474 us,
-// 1160 TFLOP/s.  The tensor core reads both operands of S from shared memory at
-// the full 128 bytes a cycle, beside the tiles' way in and, for E4M3, the
-// conversion (320 KB a step of 256 rows and 128 keys, 2560 cycles of the 3500 to
-// 4500 that a step takes); the softmax and the conversion share the issue slots.  The structure is the packed
+// 850-926 us across machines, 1160-1260 TFLOP/s; 250 tokens of 56 heads over 77000
+// E4M3 keys 474-494 us, 1115-1160 TFLOP/s.  Under ncu two chunks of 2048 tokens
+// over 8192 bf16 keys have the tensor pipe active 52% of the time (issue slots 30%,
+// the tensor core's operand reads 39% of shared memory's cycles), 250 tokens of
+// 56 heads over 40000 E4M3 keys 46% (issue slots 46%, operand reads 35% and the
+// conversion 22%): no unit is full, the softmax and the products of a half wait
+// for one another, and with two halves in flight they overlap only in part.  The
+// structure is the packed
 // forward's (varlen_fwd.cu): a unit is two halves A and B of 128 rows that share
 // every 128-key tile, S and P of a half in one TMEM region, the next S of a
 // half issued right behind its P V product, so that the tensor core works on one
@@ -29,6 +32,12 @@
 //   * Rows of V outside the unit's keys are cleared (by the converting warps, or
 //     for bf16 by warps 2 and 3) before the product reads them: they may hold
 //     anything, and 0 * NaN would poison O.
+//
+// P is rounded to bf16, V's type, which the second product asks for: each weight
+// is off by at most 2^-9 of its binade, O by 2e-3 to 2.4e-3 relative to 64 bits
+// where rounding O alone gives 1.65e-3.  The sum l takes P before that rounding.  A
+// second bf16 part, as in the kernel for few rows, would be half as many tensor
+// operations again where those are the bound.
 //
 // Warps: 0 producer, 1 MMA issuer, 2 and 3 clearing (bf16), 4..7 softmax of half
 // A, 8..11 of half B, 12..15 converting (E4M3).  The producer walks the CTA's

@@ -7,16 +7,23 @@
 // 44.7 bytes a nanosecond, 12 bf16 or 23 E4M3 elements a cycle.  The warp-level
 // m16n8k16 products take keys (then columns of V) as their 16 rows and query
 // rows as their 8 columns, S^T = K Q^T and O^T = V^T P^T: a step of 16 keys for 8
-// rows is 16 products at D = 128, and o takes 32 registers, so that enough warps
-// stay resident to hide the chain of products, softmax and products.  (The other way round, 16 query rows by 8 keys, costs twice the
-// products and registers while most of the 16 rows are empty: 214 us where this
-// form took 190 for 64 ragged E4M3 sequences, and 124 with the third CTA an SM that
-// its registers leave room for.)  Measured: 8 sequences of 17580 bf16 keys, 56
-// heads of 128, one token: 565-584 us across machines, 6.9-7.1 TB/s, the copy
-// rate.  64 E4M3 sequences of 1..8192 keys, 8 key heads: 112-118 us, 4.4-4.6 TB/s;
-// TMA delivers a row of at most 128 bytes every 5 to 6 cycles, so that half as
-// long rows come at a lower rate, and a call's fixed parts (its start, 4 us until
-// the first tile, and the join, 5 us) weigh more.
+// rows is 16 products at D = 128 (bf16 24, for P's second part), and o takes 32
+// registers, so that enough warps stay resident to hide the chain of products,
+// softmax and products.  (The other
+// way round, 16 query rows by 8 keys, costs twice the products and registers
+// while most of the 16 rows are empty: 214 us where this form took 190 for 64
+// ragged E4M3 sequences, and 124 with the third CTA an SM that its registers leave
+// room for.)
+// Measured: 8 sequences of 17580 bf16 keys, 56 heads of 128, one token: 565-585 us
+// across machines, 6.9-7.1 TB/s, the copy rate.  64 E4M3 sequences of 1..8192 keys,
+// 8 key heads: 116-120 us, 4.3-4.5 TB/s.  What holds E4M3 back, from runs in which
+// the consumers only gave the slots back (TB/s whole / stream alone): pages whose
+// rows of one head lie apart come in pieces of 128 bytes, bf16 in 256; 64 x 4096
+// keys, 8 key heads 5.1 / 5.3, with head-major pages 5.5 / 6.0, bf16 6.3 / 6.4; 8 x
+// 17580 keys, 56 heads 5.8 / 5.9 and head-major 6.5 / 6.9, bf16 6.9 / 6.9.  The
+// stream decides, then; in short calls the start (4 us until the first tile) and the
+// join (5 us) weigh besides, and among ragged lengths the ends of many short units
+// (64 of up to 8192 keys 4.4 / 5.3).
 //
 // A CTA is four consumer warps and a producer warp; two (bf16) or three (E4M3)
 // CTAs share an SM.

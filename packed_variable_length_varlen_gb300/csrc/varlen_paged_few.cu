@@ -14,9 +14,9 @@
 // while most of the 16 rows are empty: 214 us where this form took 190 for 64
 // ragged E4M3 sequences, and 124 with the third CTA an SM that its registers leave
 // room for.)
-// Measured: 8 sequences of 17580 bf16 keys, 56 heads of 128, one token: 565-585 us
+// Measured: 8 sequences of 17580 bf16 keys, 56 heads of 128, one token: 564-585 us
 // across machines, 6.9-7.1 TB/s, the copy rate.  64 E4M3 sequences of 1..8192 keys,
-// 8 key heads: 116-120 us, 4.3-4.5 TB/s.  What holds E4M3 back, from runs in which
+// 8 key heads: 115-120 us, 4.3-4.5 TB/s.  What holds E4M3 back, from runs in which
 // the consumers only gave the slots back (TB/s whole / stream alone): pages whose
 // rows of one head lie apart come in pieces of 128 bytes, bf16 in 256; 64 x 4096
 // keys, 8 key heads 5.1 / 5.3, with head-major pages 5.5 / 6.0, bf16 6.3 / 6.4; 8 x

@@ -4,7 +4,7 @@
 // Bound: 4 D operations for every visible (row, key) pair on the tensor cores;
 // the keys are read from L2 by most units.  Measured at D = 128: four chunks of
 // 1500..2048 tokens (32 heads, 8 key heads) over 4096..16384 bf16 keys, causal,
-// 850-926 us across machines, 1160-1260 TFLOP/s; 250 tokens of 56 heads over 77000
+// 850-927 us across machines, 1160-1260 TFLOP/s; 250 tokens of 56 heads over 77000
 // E4M3 keys 474-494 us, 1115-1160 TFLOP/s.  Under ncu two chunks of 2048 tokens
 // over 8192 bf16 keys have the tensor pipe active 52% of the time (issue slots 30%,
 // the tensor core's operand reads 39% of shared memory's cycles), 250 tokens of

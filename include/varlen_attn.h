@@ -32,6 +32,14 @@
  *   paged cache        varlen_attn_cache_write / _cache_read (bf16 or E4M3
  *                      pages), varlen_attn_fwd_paged (+ _workspace_size),
  *                      grouped heads, single tokens to long chunks;
+ *                      varlen_attn_fwd_paged_tree for drafted trees;
+ *   a step's lists     varlen_attn_cache_plan (+ _workspace_size): pages, slots,
+ *                      positions and masks of new rows from their numbers;
+ *                      varlen_attn_cache_move, _cache_trim: what was accepted
+ *                      stays, the rest goes;
+ *   rotary positions   varlen_attn_rotary (+ _turns) on packed rows, forward and
+ *                      gradient, varlen_attn_rotary_cache_write on the way into
+ *                      the cache;
  *   status             varlen_attn_get_device_status, _status_string,
  *                      _last_cuda_error;
  *   diagnostics        tile counts and schedules, the bounded-wait self test,
@@ -433,6 +441,179 @@ int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int32_t* cu_seq
                           int32_t total_q, int32_t num_heads, int32_t max_seqlen_q, const varlen_kv_cache* cache,
                           float scale, int32_t window_left, int32_t window_right, void* out, varlen_stride so,
                           float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of drafted trees over the cache: varlen_attn_fwd_paged for
+ * segments whose new rows see one another by a mask in place of the band.  The
+ * cache already holds the new rows: new row j of segment b (n_b rows) is
+ * position seqlens[b] - n_b + j; the positions before them are the context.
+ * Row i (packed row r) sees
+ *   - the context: all of it, or, with window_left >= 0, its positions t >=
+ *     max(positions[r], seqlens[b] - n_b) - window_left;
+ *   - new row j exactly if bit j % 32 of masks[r * mask_words + j / 32] is set
+ *     and j < n_b (bits past the last word are 0), itself included: a row whose
+ *     own bit is clear does not see itself.
+ * A row that sees nothing gets O = 0 and LSE = -inf.  Rows of the cache that no
+ * row of a segment sees may hold anything, NaN included, new ones too.
+ * masks: device uint32 [total_q][mask_words], as varlen_attn_cache_plan writes
+ * it, mask_words >= 1; positions: device int32 [total_q], read only when
+ * window_left >= 0 (then not NULL).  All other arguments, the workspace
+ * (varlen_attn_fwd_paged_workspace_size), the choice of kernels and what that
+ * may change are those of varlen_attn_fwd_paged.
+ */
+int varlen_attn_fwd_paged_tree(const void* q, varlen_stride sq, const int32_t* cu_seqlens_q, int32_t batch,
+                               int32_t total_q, int32_t num_heads, int32_t max_seqlen_q, const varlen_kv_cache* cache,
+                               float scale, const uint32_t* masks, int32_t mask_words, const int32_t* positions,
+                               int32_t window_left, void* out, varlen_stride so, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * The pages of a cache as a step hands them out and takes them back: the block
+ * table and lengths that varlen_kv_cache names (one table for the caches of all
+ * layers), and a stack of free pages.  All arrays are device memory, which the
+ * host never reads.  Sequence b owns the pages of its first
+ * ceil(seqlens[b] / page_size) table entries, no other sequence does (pages that
+ * sequences share must not come back through varlen_attn_cache_trim), and the
+ * entries behind them mean nothing.  The _out arrays receive the state after the
+ * call; each may be the array it follows or another one.
+ */
+typedef struct {
+  int32_t* block_table;      /* [batch] rows of max_pages entries */
+  const int32_t* seqlens;    /* [batch], before the call */
+  int32_t* seqlens_out;      /* [batch], after it */
+  int32_t* free_pages;       /* [num_pages]: the first *free_count are free, the last of them is taken first */
+  const int32_t* free_count; /* before the call (clamped into [0, num_pages]) */
+  int32_t* free_count_out;   /* after it */
+  int64_t table_stride;      /* entries between the rows of block_table, at least max_pages */
+  int32_t num_pages;         /* >= 1 */
+  int32_t page_size;         /* a power of two from 16 to 1024 */
+  int32_t max_pages;         /* max_pages * page_size <= 2^31 - 2048, batch * max_pages < 2^31 */
+} varlen_page_pool;
+
+/*
+ * Plans a step: from the number of new rows of every sequence (new_lens[b],
+ * negative counts as 0), packed one sequence after another,
+ *   cu_seqlens[batch + 1]  where each sequence's rows begin, clamped to `total`
+ *                          (rows past it do not exist for the call);
+ *   pages                  for positions past the pages a sequence owns, taken
+ *                          from the stack in the order of sequences and
+ *                          positions and put into its table entries;
+ *   seqlens_out            seqlens + the sequence's rows;
+ *   slots[total] (int64)   page * page_size + row of each new row's place in the
+ *                          cache, -1 for rows that have none;
+ *   positions[total]       the row's position: seqlens[b] + its index or, with
+ *                          parents, + its depth in its tree (roots have 0);
+ *   unplaced[batch]        rows of the sequence that have no place: 0, unless the
+ *                          sequence did not get its pages.
+ * Rows of the arrays behind the last sequence's get slot -1, position 0 and an
+ * empty mask, so that a step of fixed size may be captured and replayed.
+ * A sequence gets either all the pages that it needs or none: those whose running
+ * need, counted from the first sequence, exceeds the free pages, and those whose
+ * length would exceed the table, get none; their new table entries are -1 (a
+ * cache write there is dropped), their rows in pages that they own already are
+ * placed, and varlen_attn_cache_trim back to the old length undoes the step for
+ * them.  seqlens_out counts their rows all the same, as cu_seqlens does.
+ *
+ * parents (NULL: none): device int32 [total], packed like the rows: the index
+ * within its sequence of the row that each one continues, less than its own;
+ * negative for a row that continues the context.  Another value counts as
+ * negative and records VARLEN_ERR_DEVICE_BOUNDS.  Then masks [total][mask_words]
+ * receives, for each row, its own bit and those of the rows above it in its tree,
+ * as varlen_attn_fwd_paged_tree reads them.  1 <= mask_words <= 128; a sequence's
+ * rows from index 32 * mask_words on get an empty mask and depth 0, and are
+ * recorded as VARLEN_ERR_DEVICE_BOUNDS.  Without parents, masks is not read or
+ * written.
+ *
+ * batch <= 2^20.  The workspace holds varlen_attn_cache_plan_workspace_size
+ * (batch) bytes, 16-byte aligned; calls that overlap need one each.
+ */
+size_t varlen_attn_cache_plan_workspace_size(int32_t batch);
+int varlen_attn_cache_plan(const varlen_page_pool* pool, const int32_t* new_lens, int32_t batch,
+                           const int32_t* parents, int32_t total, int32_t* cu_seqlens, int64_t* slots,
+                           int32_t* positions, int32_t* unplaced, uint32_t* masks, int32_t mask_words, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Shortens sequences and gives pages back: sequence b keeps lens[b] positions or,
+ * with cu_seqlens (not NULL), its positions before the n_b = cu_seqlens[b + 1] -
+ * cu_seqlens[b] new ones and lens[b] more, clamped into [0, seqlens[b]].  Pages
+ * that this leaves empty go onto the stack, the last sequence's last page first,
+ * so that a step that is undone whole leaves the stack as it was.  Entries of -1
+ * are passed over; other entries that name no page, and pages for which the stack
+ * has no room, are recorded as VARLEN_ERR_DEVICE_BOUNDS.  The table itself is not
+ * written.  batch <= 2^20.
+ */
+int varlen_attn_cache_trim(const varlen_page_pool* pool, const int32_t* lens, const int32_t* cu_seqlens,
+                           int32_t batch, void* stream);
+
+/*
+ * Keeps the accepted rows of a step: for i < kept_lens[b] (clamped into
+ * [0, max_kept]), new row kept[b * kept_stride + i] of sequence b (an index
+ * within its n_b rows of cu_seqlens, i <= kept[..] < n_b: ascending indices are)
+ * becomes its new row i, in K, in V and in their scales.  Entries outside that
+ * range move nothing and record VARLEN_ERR_DEVICE_BOUNDS; rows whose position would be
+ * negative are passed over.  seqlens counts all n_b rows, before and after: the
+ * rest goes with varlen_attn_cache_trim.  `caches` is a host array of `count`
+ * caches (layers; at most 1024) of one shape, type and strides over one table and
+ * one seqlens (VARLEN_ERR_SHAPE otherwise); sequences that move rows must not
+ * share the pages of their new rows.  total bounds cu_seqlens as in
+ * varlen_attn_cache_write.
+ */
+int varlen_attn_cache_move(const varlen_kv_cache* caches, int32_t count, const int32_t* cu_seqlens, int32_t batch,
+                           int32_t total, const int32_t* kept, int64_t kept_stride, const int32_t* kept_lens,
+                           int32_t max_kept, void* stream);
+
+/*
+ * Rotary positions: of each head's first rotary_dim elements, pair i is turned by
+ * the angle position * f_i and scaled by `scale`:
+ *     x1' = scale (x1 cos - x2 sin),   x2' = scale (x2 cos + x1 sin);
+ * pair i is elements (i, i + rotary_dim / 2), or, interleaved, (2 i, 2 i + 1).  The
+ * elements behind rotary_dim stay as they are.  rotary_dim: a multiple of 8 from 8
+ * to head_dim.  `turns` (device, rotary_dim / 2 entries, 8-byte aligned) holds f_i as a
+ * fraction of a turn a position in units of 2^-64, so that the angle of any int32
+ * position is exact to 2^-32 of a turn; varlen_attn_rotary_turns (host memory on
+ * both sides) makes it from frequencies in radians a position, however these were
+ * scaled for long contexts.  The struct is host memory, read during the call only.
+ */
+typedef struct {
+  const uint64_t* turns;
+  int32_t rotary_dim;
+  int32_t interleaved; /* 0 or 1 */
+  float scale;         /* finite */
+} varlen_rotary;
+
+int varlen_attn_rotary_turns(const double* frequencies, int32_t count, uint64_t* turns);
+
+/*
+ * Turns packed rows q [total, num_heads, head_dim] and k [total, num_kv_heads,
+ * head_dim] (bf16; num_kv_heads = 0: none, k and k_out are not looked at) into q_out
+ * and k_out.  Products are in fp32 and rounded once.  inverse != 0 turns back: with
+ * the same scale, the gradient with respect to q and k from that with respect to
+ * q_out and k_out.  Row r stands at positions[r] (device int32, any value) or, where
+ * positions is NULL, at its index within its segment of cu_seqlens; rows outside every
+ * segment are then not written.  An output may be its own input (the same address
+ * and strides; VARLEN_ERR_STRIDE for other strides at that address); other overlaps
+ * race.
+ */
+int varlen_attn_rotary(const void* q, varlen_stride sq, const void* k, varlen_stride sk, const int32_t* positions,
+                       const int32_t* cu_seqlens, int32_t batch, int32_t total, int32_t num_heads,
+                       int32_t num_kv_heads, int32_t head_dim, const varlen_rotary* rotary, int32_t inverse,
+                       void* q_out, varlen_stride sqo, void* k_out, varlen_stride sko, void* stream);
+
+/*
+ * The new rows of a step on their way into the cache, in one kernel: q is turned into
+ * q_out as by varlen_attn_rotary (in place if they are the same), k is turned, and k
+ * and v go to the cache's slots[r] (device int64, page * page_size + row, as
+ * varlen_attn_cache_plan writes them): the bits that varlen_attn_rotary followed by
+ * varlen_attn_cache_write would leave.  Negative slots are passed over; slots past the
+ * last page are too, and record VARLEN_ERR_DEVICE_BOUNDS.  Two rows with one slot race.
+ * positions is required; the cache's block_table, seqlens and max_pages are not looked
+ * at.  num_heads = 0: no queries.
+ */
+int varlen_attn_rotary_cache_write(const void* q, varlen_stride sq, const void* k, varlen_stride sk, const void* v,
+                                   varlen_stride sv, const int32_t* positions, const int64_t* slots, int32_t total,
+                                   int32_t num_heads, const varlen_kv_cache* cache, const varlen_rotary* rotary,
+                                   void* q_out, varlen_stride sqo, void* stream);
 
 /*
  * Backward without a workspace argument, for callers that cannot allocate

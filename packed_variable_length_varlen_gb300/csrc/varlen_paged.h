@@ -35,6 +35,17 @@ struct PageView {
   int32_t num_pages, max_pages, page_size, page_shift;
 };
 
+// ------------------------------------------------- from varlen_paged_api.cu
+// Argument checks of a cache; `lists`: of its table and lengths too.
+int check_cache(const varlen_kv_cache* cache, int32_t batch, bool lists, int* page_shift);
+// Log2 of a page size, -1 for one that is not allowed.
+int page_shift_of(int32_t page_size);
+// Bytes of an element, of a page array and of a scale array.
+int elem_bytes(const varlen_kv_cache& c);
+int64_t pages_bytes(const varlen_kv_cache& c, varlen_page_stride s);
+int64_t scale_bytes(const varlen_kv_cache& c);
+PageView view_of(const varlen_kv_cache& c, int shift);
+
 // Positions sequence b holds, clamped to what its table row can name.
 __device__ __forceinline__ int32_t cache_len(const PageView& c, int32_t b) {
   const int64_t cap = (int64_t)c.max_pages << c.page_shift;
@@ -102,8 +113,13 @@ struct PagedParams {
   int64_t win_left, win_right;
   float scale_log2;
   unsigned int* err;
+  // drafted trees (their kernels only): which of the segment's new rows each row
+  // sees, and where it stands (read with a bounded win_left)
+  const uint32_t* masks;
+  const int32_t* tree_pos;
+  int32_t mask_words;
   int32_t debug_skip_few, debug_skip_many;  // < 0: off; else CTA 0's producer skips its load number n (failure test)
-  Span q_span, out_span, lse_span;  // bounds-checking build
+  Span q_span, out_span, lse_span, masks_span, pos_span;  // bounds-checking build
 };
 
 // What a kernel takes: segments of at most kFewRows rows, of more, or all.
@@ -146,7 +162,7 @@ struct PagedParts {
 struct PagedLaunch {
   PagedParams p;
   int head_dim, sms;
-  bool e4m3;
+  bool e4m3, tree;
   bool few, many;  // which kernels run; alone, each takes every segment
   CUtensorMap few_k, few_v, few_ks, few_vs;  // pages and (E4M3) scales in boxes of up to kFewTile keys
   CUtensorMap chunk_q;                       // {D, group, key heads, rows}, boxes of half a unit

@@ -11,10 +11,7 @@
 
 using namespace varlen;
 
-namespace {
-
-constexpr int32_t kMaxBatch = 1 << 30;  // strides over the batch stay in int32
-constexpr float kLog2e = 1.4426950408889634f;
+namespace varlen {
 
 int elem_bytes(const varlen_kv_cache& c) { return c.type == VARLEN_CACHE_BF16 ? 2 : 1; }
 
@@ -24,6 +21,19 @@ int64_t pages_bytes(const varlen_kv_cache& c, varlen_page_stride s) {
   return elem_bytes(c) * (page + row + (c.num_kv_heads > 1 ? (c.num_kv_heads - 1) * s.head : 0) + c.head_dim);
 }
 int64_t scale_bytes(const varlen_kv_cache& c) { return (int64_t)2 * c.num_pages * c.num_kv_heads * c.page_size; }
+
+int page_shift_of(int32_t page_size) {
+  for (int shift = 4; shift <= 10; ++shift)
+    if ((1 << shift) == page_size) return shift;
+  return -1;
+}
+
+}  // namespace varlen
+
+namespace {
+
+constexpr int32_t kMaxBatch = 1 << 30;  // strides over the batch stay in int32
+constexpr float kLog2e = 1.4426950408889634f;
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -46,18 +56,22 @@ int check_pages(const varlen_kv_cache& c, varlen_page_stride s) {
   return VARLEN_OK;
 }
 
-int check_cache(const varlen_kv_cache* cache, int32_t batch, int* page_shift) {
+}  // namespace
+
+namespace varlen {
+
+int check_cache(const varlen_kv_cache* cache, int32_t batch, bool lists, int* page_shift) {
   if (cache == nullptr) return VARLEN_ERR_NULL;
   const varlen_kv_cache& c = *cache;
-  if (batch < 1 || batch > kMaxBatch || c.num_pages < 1 || c.max_pages < 0 || c.num_kv_heads < 1 || c.table_stride < 0) return VARLEN_ERR_SHAPE;
+  if (c.num_pages < 1 || c.num_kv_heads < 1) return VARLEN_ERR_SHAPE;
+  if (lists && (batch < 1 || batch > kMaxBatch || c.max_pages < 0 || c.table_stride < 0)) return VARLEN_ERR_SHAPE;
   if (c.type != VARLEN_CACHE_BF16 && c.type != VARLEN_CACHE_E4M3) return VARLEN_ERR_SHAPE;
-  int shift = 4;
-  while (shift < 11 && (1 << shift) != c.page_size) ++shift;
-  if (shift == 11) return VARLEN_ERR_SHAPE;
-  if (((int64_t)c.max_pages << shift) > (int64_t(1) << 31) - 2048) return VARLEN_ERR_SHAPE;  // tile ends stay in int32
+  const int shift = page_shift_of(c.page_size);
+  if (shift < 0) return VARLEN_ERR_SHAPE;
+  if (lists && ((int64_t)c.max_pages << shift) > (int64_t(1) << 31) - 2048) return VARLEN_ERR_SHAPE;  // tile ends stay in int32
   if (c.head_dim != 64 && c.head_dim != 96 && c.head_dim != 128) return VARLEN_ERR_HEAD_DIM;
-  if (c.k == nullptr || c.v == nullptr || c.seqlens == nullptr || (c.max_pages > 0 && c.block_table == nullptr))
-    return VARLEN_ERR_NULL;
+  if (c.k == nullptr || c.v == nullptr) return VARLEN_ERR_NULL;
+  if (lists && (c.seqlens == nullptr || (c.max_pages > 0 && c.block_table == nullptr))) return VARLEN_ERR_NULL;
   const bool scaled = c.type == VARLEN_CACHE_E4M3;
   if (scaled && (c.k_scale == nullptr || c.v_scale == nullptr)) return VARLEN_ERR_NULL;
   if (!aligned(c.k, 16) || !aligned(c.v, 16) || (scaled && (!aligned(c.k_scale, 16) || !aligned(c.v_scale, 16))))
@@ -71,6 +85,10 @@ int check_cache(const varlen_kv_cache* cache, int32_t batch, int* page_shift) {
 PageView view_of(const varlen_kv_cache& c, int shift) {
   return PageView{c.block_table, c.table_stride, c.seqlens, c.num_pages, c.max_pages, c.page_size, shift};
 }
+
+}  // namespace varlen
+
+namespace {
 
 // Pages as {D, heads, page rows, pages} in boxes of 128 bytes (64 bf16 or 128
 // codes, zero past D) of `rows` rows of one head and page.
@@ -109,7 +127,7 @@ int encode_queries(CUtensorMap* map, const void* base, varlen_stride s, int32_t 
 int cache_impl(const void* k, varlen_stride sk, const void* v, varlen_stride sv, const int32_t* cu, int32_t batch,
                int32_t total, const varlen_kv_cache* cache, void* stream, bool write) {
   int shift = 0;
-  int st = check_cache(cache, batch, &shift);
+  int st = check_cache(cache, batch, true, &shift);
   if (st != VARLEN_OK) return st;
   if (total < 0) return VARLEN_ERR_SHAPE;
   if (cu == nullptr) return VARLEN_ERR_NULL;
@@ -184,13 +202,21 @@ extern "C" size_t varlen_attn_fwd_paged_workspace_size(int32_t batch, int32_t to
   return paged_workspace((int64_t)total_q * (num_heads / num_kv_heads), head_dim).bytes;
 }
 
-extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int32_t* cu_seqlens_q, int32_t batch,
-                                     int32_t total_q, int32_t num_heads, int32_t max_seqlen_q,
-                                     const varlen_kv_cache* cache, float scale, int32_t window_left,
-                                     int32_t window_right, void* out, varlen_stride so, float* lse, void* workspace,
-                                     size_t workspace_bytes, void* stream) {
+namespace {
+
+// Drafted trees: what replaces the band.
+struct TreeArgs {
+  const uint32_t* masks;
+  int32_t mask_words;
+  const int32_t* positions;
+};
+
+int fwd_paged_impl(const void* q, varlen_stride sq, const int32_t* cu_seqlens_q, int32_t batch, int32_t total_q,
+                   int32_t num_heads, int32_t max_seqlen_q, const varlen_kv_cache* cache, float scale,
+                   int32_t window_left, int32_t window_right, const TreeArgs* tree, void* out, varlen_stride so,
+                   float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   int shift = 0;
-  int st = check_cache(cache, batch, &shift);
+  int st = check_cache(cache, batch, true, &shift);
   if (st != VARLEN_OK) return st;
   const varlen_kv_cache& c = *cache;
   if (total_q < 0 || num_heads < 1 || num_heads % c.num_kv_heads != 0 || num_heads / c.num_kv_heads > 128)
@@ -202,6 +228,11 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   if ((total_q > 1 && sq.row == 0) || (num_heads > 1 && sq.head == 0)) return VARLEN_ERR_STRIDE;
   if ((st = check_nhd(out, so, total_q, num_heads, c.head_dim, true)) != VARLEN_OK) return st;
   if (total_q > 0 && lse == nullptr) return VARLEN_ERR_NULL;
+  if (tree != nullptr) {
+    if (tree->mask_words < 1 || tree->mask_words > (1 << 20)) return VARLEN_ERR_SHAPE;
+    if (total_q > 0 && (tree->masks == nullptr || (window_left >= 0 && tree->positions == nullptr))) return VARLEN_ERR_NULL;
+    if (!aligned(tree->masks, 4) || !aligned(tree->positions, 4)) return VARLEN_ERR_ALIGN;
+  }
   const size_t need = varlen_attn_fwd_paged_workspace_size(batch, total_q, num_heads, c.num_kv_heads, c.head_dim);
   if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need) return VARLEN_ERR_WORKSPACE;
   int sms = 0;
@@ -227,6 +258,14 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   p.win_left = window_left < 0 ? kWinUnbounded : window_left;
   p.win_right = window_right < 0 ? kWinUnbounded : window_right;
   p.scale_log2 = scale * kLog2e;
+  if (tree != nullptr) {
+    L.tree = true;
+    p.masks = tree->masks;
+    p.mask_words = tree->mask_words;
+    p.tree_pos = tree->positions;
+    p.masks_span = checked_span(tree->masks, (int64_t)total_q * tree->mask_words * 4);
+    p.pos_span = checked_span(tree->positions, (int64_t)total_q * 4);
+  }
   p.err = err;
   paged_skip_knobs(&p.debug_skip_few, &p.debug_skip_many);
   p.q_span = nhd_bytes(q, sq, total_q, num_heads, c.head_dim);
@@ -277,4 +316,26 @@ extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int3
   }
   const cudaError_t e = launch_paged(L, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VARLEN_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int32_t* cu_seqlens_q, int32_t batch,
+                                     int32_t total_q, int32_t num_heads, int32_t max_seqlen_q,
+                                     const varlen_kv_cache* cache, float scale, int32_t window_left,
+                                     int32_t window_right, void* out, varlen_stride so, float* lse, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  return fwd_paged_impl(q, sq, cu_seqlens_q, batch, total_q, num_heads, max_seqlen_q, cache, scale, window_left,
+                        window_right, nullptr, out, so, lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" int varlen_attn_fwd_paged_tree(const void* q, varlen_stride sq, const int32_t* cu_seqlens_q, int32_t batch,
+                                          int32_t total_q, int32_t num_heads, int32_t max_seqlen_q,
+                                          const varlen_kv_cache* cache, float scale, const uint32_t* masks,
+                                          int32_t mask_words, const int32_t* positions, int32_t window_left, void* out,
+                                          varlen_stride so, float* lse, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+  const TreeArgs tree{masks, mask_words, positions};
+  return fwd_paged_impl(q, sq, cu_seqlens_q, batch, total_q, num_heads, max_seqlen_q, cache, scale, window_left, -1,
+                        &tree, out, so, lse, workspace, workspace_bytes, stream);
 }

@@ -50,7 +50,8 @@ namespace varlen {
 
 namespace {
 
-using ChunkGeom = PagedGeom<kChunkRows, kChunkTile, true>;
+template <bool TREE>
+using ChunkGeomOf = PagedGeom<kChunkRows, kChunkTile, true, TREE>;
 
 constexpr int kLeastTiles = 2;  // tiles per CTA when there are few
 constexpr int kPieces = 4;      // pieces that the producer may be ahead
@@ -104,18 +105,25 @@ struct PieceReader {
   }
 };
 
+// any[k] without an array in memory.
+__device__ __forceinline__ uint32_t any_of(const uint32_t (&any)[4], int k) {
+  const uint32_t lo = (k & 1) ? any[1] : any[0], hi = (k & 1) ? any[3] : any[2];
+  return (k & 2) ? hi : lo;
+}
+
 __device__ __forceinline__ uint32_t mul_pair(uint32_t a, uint32_t b) {
   const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool TREE>
 __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
     varlen_paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_ks,
                               const __grid_constant__ CUtensorMap tm_vs, const PagedParams p, const PagedParts parts,
                               int32_t take) {
   using C = ChunkCfg<D, E4M3>;
+  using ChunkGeom = ChunkGeomOf<TREE>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_addr(smem) & 1023u) != 0) {
     paged_refuse(p, parts);
@@ -340,13 +348,24 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
       const int t = threadIdx.x - 64;  // 0..63
       while (ok && pieces.next(sh, x, abort)) {
         const int32_t tiles = min(x.j1, x.u.tiles);
+        const int32_t unit_lo = TREE ? tree_unit_lo(p, x) : x.u.lo;
         for (int32_t j = x.j0; j < tiles; ++j, pos += 2) {
           const uint32_t vpos = pos + 1, s = vpos % C::NSLOT;
           if (!mbar_wait_warp(&sh.kv_full[s], (vpos / C::NSLOT) & 1, abort)) { ok = false; break; }
           const int32_t key0 = (x.u.tile0 + j) * kChunkTile;
-          const int lo = max(x.u.lo - key0, 0), hi = min(x.u.hi - key0, kChunkTile);
-          if (lo > 0 || hi < kChunkTile) {
-            uint4* base = reinterpret_cast<uint4*>(ring + s * C::TILE);
+          const int lo = max(unit_lo - key0, 0), hi = min(x.u.hi - key0, kChunkTile);
+          uint4* base = reinterpret_cast<uint4*>(ring + s * C::TILE);
+          if (TREE && key0 + kChunkTile > x.sk - x.n) {
+            uint32_t any[4];
+            tree_unit_bits(p, x, unit_lo, key0, any);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              for (int u = t; any[k] != ~0u && u < 32 * 8; u += 64)
+                if (((any[k] >> (u >> 3)) & 1u) == 0)
+#pragma unroll
+                  for (int c = 0; c < C::NC; ++c) base[c * (C::CHUNK / 16) + k * 256 + u] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          } else if (lo > 0 || hi < kChunkTile) {
 #pragma unroll
             for (int c = 0; c < C::NC; ++c) {
               for (int u = t; u < lo * 8; u += 64) base[c * (C::CHUNK / 16) + u] = make_uint4(0, 0, 0, 0);
@@ -382,7 +401,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
       // a row that is none sees all keys: what it computes goes nowhere, and its
       // warp is spared the selects
       int32_t key_lo = 0, key_hi = INT32_MAX;
-      if (live) band_keys(tok, tok, x.n, x.sk, p.win_left, p.win_right, &key_lo, &key_hi);
+      if (live && TREE) {
+        key_lo = tree_lo(p, orow, x.sk - x.n);
+        key_hi = x.sk;
+      } else if (live) {
+        band_keys(tok, tok, x.n, x.sk, p.win_left, p.win_right, &key_lo, &key_hi);
+      }
       const int32_t key0 = (x.u.tile0 + x.j0) * kChunkTile;
       for (int32_t j = 0; j < tiles; ++j) {
         if (!mbar_wait_warp(&sh.s_full[hf], (g + j) & 1, abort)) { ok = false; break; }
@@ -405,7 +429,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(s[i]);
         // keys that the row does not see are set to -inf by select
         const int32_t lim = key_hi - (key0 + j * kChunkTile), lim_lo = key_lo - (key0 + j * kChunkTile);
-        if (__any_sync(0xffffffffu, lim_lo > 0)) {
+        if (TREE && key0 + (j + 1) * kChunkTile > x.sk - x.n) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int32_t rel = key0 + j * kChunkTile + 32 * k - (x.sk - x.n);
+            const uint32_t see = (live ? tree_bits(p, orow, rel) : ~0u) & bits_between(lim_lo - 32 * k, lim - 32 * k);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[32 * k + i] = (see & (1u << i)) != 0 ? v[32 * k + i] : -INFINITY;
+          }
+        } else if (__any_sync(0xffffffffu, lim_lo > 0)) {
 #pragma unroll
           for (int i = 0; i < 128; ++i) v[i] = (i < lim && i >= lim_lo) ? v[i] : -INFINITY;
         } else if (__any_sync(0xffffffffu, lim < kChunkTile)) {
@@ -530,6 +562,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
     bool ok = true;
     while (ok && pieces.next(sh, x, abort)) {
       const int32_t tiles = min(x.j1, x.u.tiles);
+      const int32_t unit_lo = TREE ? tree_unit_lo(p, x) : x.u.lo;
       for (int32_t j = x.j0; ok && j < tiles; ++j) {
         const int32_t key0 = (x.u.tile0 + j) * kChunkTile;
 #pragma unroll 1
@@ -542,13 +575,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
           const uint8_t* sc = scales + rs * C::SCALES;
           uint8_t* dst = ring + s * C::TILE;
           // rows of V that no row of the unit sees may hold anything: cleared
-          const int lo = which ? x.u.lo - key0 : -1, hi = which ? x.u.hi - key0 : kChunkTile;
+          const int lo = which ? unit_lo - key0 : -1, hi = which ? x.u.hi - key0 : kChunkTile;
+          uint32_t any[4] = {~0u, ~0u, ~0u, ~0u};
+          if (TREE && which && key0 + kChunkTile > x.sk - x.n) tree_unit_bits(p, x, unit_lo, key0, any);
 #pragma unroll
           for (int i = 0; i < C::NC; ++i) {
             const int r = r0 + i * 64;
             const float f = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
                 sc + ((r >> box_shift) << 7) + ((r & ((1 << box_shift) - 1)) << 1)));
-            const bool keep = r >= lo && r < hi, large = keep && f > 0x1p7f;
+            const bool keep = r >= lo && r < hi && (!TREE || ((any_of(any, r >> 5) >> (r & 31)) & 1u) != 0), large = keep && f > 0x1p7f;
             // 2^120 * scale, 0 for a row to clear (the codes' bits are finite in any case)
             const float f1 = keep ? (large ? 0x1p127f : f * 0x1p120f) : 0.f;
             const uint32_t ff = pack_bf16x2(f1, f1);
@@ -597,10 +632,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
   if (threadIdx.x == 0 && sh.abort) record_error(p.err, kErrTimeout);
 }
 
-template <int D, bool E4M3>
-cudaError_t launch_chunk_d(const PagedLaunch& L, int32_t take, cudaStream_t stream) {
+template <int D, bool E4M3, bool TREE>
+cudaError_t launch_chunk_as(const PagedLaunch& L, int32_t take, cudaStream_t stream) {
   using C = ChunkCfg<D, E4M3>;
-  auto kern = varlen_paged_chunk_kernel<D, E4M3>;
+  auto kern = varlen_paged_chunk_kernel<D, E4M3, TREE>;
   // The register split assumes the compiled per-thread count; refuse to
   // launch a build that came out differently.
   cudaFuncAttributes fa;
@@ -611,6 +646,11 @@ cudaError_t launch_chunk_d(const PagedLaunch& L, int32_t take, cudaStream_t stre
   if (e != cudaSuccess) return e;
   return launch_overlapped(kern, (unsigned)L.sms, C::THREADS, C::SMEM, stream, L.chunk_q, L.chunk_k, L.chunk_v, L.chunk_ks,
                            L.chunk_vs, L.p, L.chunk, take);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_chunk_d(const PagedLaunch& L, int32_t take, cudaStream_t stream) {
+  return L.tree ? launch_chunk_as<D, E4M3, true>(L, take, stream) : launch_chunk_as<D, E4M3, false>(L, take, stream);
 }
 
 }  // namespace

@@ -85,7 +85,6 @@ struct FewCfg {
   static constexpr int KT = kFewTile;                       // keys per tile
   static constexpr int STEP = 16;                           // keys a warp takes at a time
   static constexpr int ROWS = kFewRows;
-  using Geom = PagedGeom<ROWS, KT, false>;
   static constexpr int CK = E4M3 ? 1 : (D + 63) / 64;       // 128-byte column chunks of a row
   static constexpr int CHUNK = KT * 128;
   static constexpr int TILE = CK * CHUNK;
@@ -184,12 +183,13 @@ __device__ __forceinline__ uint32_t scale_at(uint32_t r, int shift) {
   return ((r >> shift) << 7) + ((r & ((1u << shift) - 1)) << 1);
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool TREE>
 __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
     varlen_paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                             const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
                             const PagedParams p, const PagedParts parts, int32_t take) {
   using C = FewCfg<D, E4M3>;
+  using Geom = PagedGeom<C::ROWS, C::KT, false, TREE>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_addr(smem) & 1023u) != 0) {
     paged_refuse(p, parts);
@@ -211,9 +211,9 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
     fence_barrier_init();
   }
   dependency_wait();  // nothing above reads or writes global memory
-  paged_start<typename C::Geom>(sh.start, p, take, kLeastTiles);
+  paged_start<Geom>(sh.start, p, take, kLeastTiles);
   dependents_may_launch();
-  PagedWalk<typename C::Geom> walk;
+  PagedWalk<Geom> walk;
   PagedPiece x;
   const int box_shift = min(p.pages.page_shift, 6);  // keys of one page piece of a tile
 
@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         tok[i] = x.u.t0 + (skip + min(rt * 8 + 2 * c + i, rows - 1)) / p.group;
-        band_keys(tok[i], tok[i], x.n, x.sk, p.win_left, p.win_right, &klo[i], &khi[i]);
+        if constexpr (TREE) klo[i] = tree_lo(p, (int64_t)x.q0 + tok[i], x.sk - x.n);
+        else band_keys(tok[i], tok[i], x.n, x.sk, p.win_left, p.win_right, &klo[i], &khi[i]);
       }
       uint32_t qf[C::KSTEPS][2];
       float rowf[2] = {p.scale_log2, p.scale_log2};
@@ -332,7 +333,12 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
       for (int t = 0; t < C::MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
       // keys that every row of the unit sees: no select needed
       int32_t all_lo, all_hi;
-      {
+      if constexpr (TREE) {
+        all_lo = max(klo[0], klo[1]);
+        all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, 1));
+        all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, 2));
+        all_hi = x.sk - x.n;
+      } else {
         int32_t a, e;
         band_keys(x.u.t1, x.u.t1, x.n, x.sk, p.win_left, p.win_right, &all_lo, &e);
         band_keys(x.u.t0, x.u.t0, x.n, x.sk, p.win_left, p.win_right, &a, &all_hi);
@@ -357,12 +363,13 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
         const int32_t key0 = (x.u.tile0 + j) * C::KT;
         const bool edge = key0 < all_lo || key0 + C::KT > all_hi;
         // rows of V that no row of the unit sees may hold anything: cleared
-        const bool vedge = key0 < x.u.lo || key0 + C::KT > x.u.hi;
+        const bool vedge = TREE ? edge : key0 < x.u.lo || key0 + C::KT > x.u.hi;
         bool v_here = false;
         // the steps of this warp: kg, kg + share, ...
 #pragma unroll 1
         for (int a = kg * C::STEP; a < C::KT; a += share * C::STEP) {
           float s[4], s2[4];  // keys a + r and a + r + 8 of rows 2c, 2c + 1; s2: a second chain of products
+          uint32_t seen0 = 0, seen1 = 0;  // TREE: lanes that see one of their keys a + r, a + r + 8
           {
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[e] = s2[e] = 0.f;
@@ -407,7 +414,19 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
             if (lane == 0) mbar_arrive(&sh.empty[ks]);
           }
           {
-            if (edge) {
+            if (TREE && edge) {
+              bool any[2] = {false, false};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int32_t key = key0 + a + r + (e >> 1) * 8, rel = key - (x.sk - x.n);
+                const bool see = rel < 0 ? key >= klo[e & 1]
+                                         : rel < x.n && ((tree_word_at(p, (int64_t)x.q0 + tok[e & 1], rel >> 5) >> (rel & 31)) & 1u) != 0;
+                s[e] = see ? s[e] : -INFINITY;
+                any[e >> 1] = any[e >> 1] || see;
+              }
+              seen0 = __ballot_sync(0xffffffffu, any[0]);
+              seen1 = __ballot_sync(0xffffffffu, any[1]);
+            } else if (edge) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int32_t key = key0 + a + r + (e >> 1) * 8;
@@ -455,7 +474,11 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
           __syncwarp();
           uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;  // keys 2c, 2c+1 and 2c+8, 2c+9
           if (vedge) {
-            auto in = [&](int k) { return key0 + a + k >= x.u.lo && key0 + a + k < x.u.hi; };
+            // (TREE: a key's four lanes stand next to one another)
+            auto in = [&](int k) {
+              if (TREE) return ((k < 8 ? seen0 >> (4 * k) : seen1 >> (4 * k - 32)) & 0xfu) != 0;
+              return key0 + a + k >= x.u.lo && key0 + a + k < x.u.hi;
+            };
             keep0 = (in(2 * c) ? 0xffffu : 0u) | (in(2 * c + 1) ? 0xffff0000u : 0u);
             keep1 = (in(2 * c + 8) ? 0xffffu : 0u) | (in(2 * c + 9) ? 0xffff0000u : 0u);
           }
@@ -485,8 +508,11 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
             for (int k = 0; k < 2; ++k) sv[k] = __bfloat162float(lds<__nv_bfloat16>(vsc + scale_at(a + r + 8 * k, box_shift)));
             if (vedge) {
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
-                sv[k] = key0 + a + r + 8 * k >= x.u.lo && key0 + a + r + 8 * k < x.u.hi ? sv[k] : 0.f;
+              for (int k = 0; k < 2; ++k) {
+                const bool in = TREE ? (((k ? seen1 : seen0) >> (4 * r)) & 0xfu) != 0
+                                     : key0 + a + r + 8 * k >= x.u.lo && key0 + a + r + 8 * k < x.u.hi;
+                sv[k] = in ? sv[k] : 0.f;
+              }
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const bool keep = ((k >> 1) ? keep1 : keep0) & ((k & 1) ? 0xffff0000u : 0xffffu);
@@ -711,14 +737,19 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
   if (threadIdx.x == 0 && sh.abort) record_error(p.err, kErrTimeout);
 }
 
-template <int D, bool E4M3>
-cudaError_t launch_few_d(const PagedLaunch& L, int32_t take, cudaStream_t stream) {
+template <int D, bool E4M3, bool TREE>
+cudaError_t launch_few_as(const PagedLaunch& L, int32_t take, cudaStream_t stream) {
   using C = FewCfg<D, E4M3>;
-  auto kern = varlen_paged_few_kernel<D, E4M3>;
+  auto kern = varlen_paged_few_kernel<D, E4M3, TREE>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_overlapped(kern, (unsigned)(L.sms * few_ctas(E4M3)), C::THREADS, C::SMEM, stream, L.few_k, L.few_v, L.few_ks,
                            L.few_vs, L.p, L.few_parts, take);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_few_d(const PagedLaunch& L, int32_t take, cudaStream_t stream) {
+  return L.tree ? launch_few_as<D, E4M3, true>(L, take, stream) : launch_few_as<D, E4M3, false>(L, take, stream);
 }
 
 }  // namespace

@@ -38,8 +38,9 @@ struct PagedUnit {
 
 // Geometry of a kernel's units: ROWS rows per block, or, with BY_TOKEN, the
 // rows of two halves of whole tokens (ROWS / 2 / group tokens each); TILE keys
-// per tile.
-template <int ROWS, int TILE, bool BY_TOKEN>
+// per tile.  TREE: the keys are those from where a row at the context's end would
+// begin to see them to the last new row, whichever of them the masks name.
+template <int ROWS, int TILE, bool BY_TOKEN, bool TREE>
 struct PagedGeom {
   __device__ static __forceinline__ int32_t half_tokens(const PagedParams& p) { return ROWS / 2 / p.group; }
   __device__ static __forceinline__ int32_t blocks(const PagedParams& p, int32_t n) {
@@ -57,7 +58,8 @@ struct PagedGeom {
       u.t0 = (int32_t)(r0 / (uint32_t)p.group);
       u.t1 = (int32_t)(r1 / (uint32_t)p.group);
     }
-    band_keys(u.t0, u.t1, n, sk, p.win_left, p.win_right, &u.lo, &u.hi);
+    if (TREE) band_keys(0, 0, n, sk, p.win_left, kWinUnbounded, &u.lo, &u.hi);
+    else band_keys(u.t0, u.t1, n, sk, p.win_left, p.win_right, &u.lo, &u.hi);
     u.tile0 = u.lo / TILE;
     u.tiles = u.hi > u.lo ? (u.hi - 1) / TILE + 1 - u.tile0 : 0;
     return u;
@@ -262,6 +264,58 @@ struct PagedWalk {
     return true;
   }
 };
+
+// ------------------------------------------------- drafted trees
+// ctx: position of a segment's new row 0 (its keys less its new rows; negative
+// where rows are missing).  A row sees the keys [tree_lo, ctx) and those new rows j,
+// key ctx + j, whose bit its mask has.
+__device__ __forceinline__ int32_t tree_lo(const PagedParams& p, int64_t row, int32_t ctx) {
+  if (p.win_left >= kWinUnbounded) return 0;
+  const int32_t* a = p.tree_pos + row;
+  const int64_t at = in_span(p.pos_span, a, 4, p.err) ? *a : 0;
+  // (a row whose window begins behind the context sees none of it: ctx)
+  return (int32_t)max(min(max(at, (int64_t)ctx) - p.win_left, (int64_t)ctx), (int64_t)0);
+}
+
+__device__ __forceinline__ uint32_t tree_word_at(const PagedParams& p, int64_t row, int32_t w) {
+  const uint32_t* a = p.masks + row * p.mask_words + w;
+  return (uint32_t)w < (uint32_t)p.mask_words && in_span(p.masks_span, a, 4, p.err) ? *a : 0u;
+}
+
+// 32 bits of a packed row's mask, from new row `rel` on; those before new row 0
+// (the context's) are set.
+__device__ __forceinline__ uint32_t tree_bits(const PagedParams& p, int64_t row, int32_t rel) {
+  if (rel <= -32) return ~0u;
+  if (rel < 0) return (tree_word_at(p, row, 0) << -rel) | ((1u << -rel) - 1u);
+  const uint32_t lo = tree_word_at(p, row, rel >> 5);
+  return (rel & 31) == 0 ? lo : __funnelshift_r(lo, tree_word_at(p, row, (rel >> 5) + 1), rel & 31);
+}
+
+// Bits [lo, hi) of a word.
+__device__ __forceinline__ uint32_t bits_between(int32_t lo, int32_t hi) {
+  const uint32_t below = hi >= 32 ? ~0u : (hi <= 0 ? 0u : (1u << hi) - 1u);
+  return lo <= 0 ? below : (lo >= 32 ? 0u : below & ~((1u << lo) - 1u));
+}
+
+// A whole warp: the first key that some row of the unit sees of the context.
+__device__ __forceinline__ int32_t tree_unit_lo(const PagedParams& p, const PagedPiece& x) {
+  if (p.win_left >= kWinUnbounded) return x.u.lo;
+  int32_t lo = INT32_MAX;
+  for (int32_t t = x.u.t0 + (int32_t)(threadIdx.x & 31); t <= x.u.t1; t += 32) lo = min(lo, tree_lo(p, (int64_t)x.q0 + t, x.sk - x.n));
+  return max(__reduce_min_sync(0xffffffffu, lo), x.u.lo);
+}
+
+// A whole warp: which of the 128 keys from key0 on some row of the unit sees.
+__device__ __forceinline__ void tree_unit_bits(const PagedParams& p, const PagedPiece& x, int32_t unit_lo, int32_t key0, uint32_t (&any)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) any[k] = 0;
+  for (int32_t t = x.u.t0 + (int32_t)(threadIdx.x & 31); t <= x.u.t1; t += 32)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) any[k] |= tree_bits(p, (int64_t)x.q0 + t, key0 + 32 * k - (x.sk - x.n));
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    any[k] = __reduce_or_sync(0xffffffffu, any[k]) & bits_between(unit_lo - key0 - 32 * k, x.u.hi - key0 - 32 * k);
+}
 
 // Entry i of the join's list.
 __device__ __forceinline__ void put_join(const PagedParams& p, const PagedParts& parts, int32_t i, const PagedJoin& u) {

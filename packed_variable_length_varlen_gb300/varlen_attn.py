@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 
 import torch
@@ -54,6 +55,20 @@ class VarlenKvCache(ctypes.Structure):
                 ("sk", VarlenPageStride), ("sv", VarlenPageStride), ("table_stride", ctypes.c_int64),
                 ("type", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class VarlenPagePool(ctypes.Structure):
+    """varlen_page_pool of the C header."""
+    _fields_ = [("block_table", ctypes.c_void_p), ("seqlens", ctypes.c_void_p), ("seqlens_out", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p), ("free_count_out", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
+
+
+class VarlenRotary(ctypes.Structure):
+    """varlen_rotary of the C header."""
+    _fields_ = [("turns", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 VARLEN_CACHE_BF16 = 0
@@ -128,6 +143,23 @@ def _load() -> ctypes.CDLL:
     lib.varlen_attn_fwd_paged_workspace_size.argtypes = [i32, i32, i32, i32, i32]
     lib.varlen_attn_fwd_paged.restype = ctypes.c_int
     lib.varlen_attn_fwd_paged.argtypes = [vp, S, vp, i32, i32, i32, i32, vp, f32, i32, i32, vp, S, vp, vp, sz, vp]
+    lib.varlen_attn_fwd_paged_tree.restype = ctypes.c_int
+    lib.varlen_attn_fwd_paged_tree.argtypes = [vp, S, vp, i32, i32, i32, i32, vp, f32, vp, i32, vp, i32, vp, S, vp, vp, sz,
+                                               vp]
+    lib.varlen_attn_cache_plan_workspace_size.restype = sz
+    lib.varlen_attn_cache_plan_workspace_size.argtypes = [i32]
+    lib.varlen_attn_cache_plan.restype = ctypes.c_int
+    lib.varlen_attn_cache_plan.argtypes = [vp, vp, i32, vp, i32, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+    lib.varlen_attn_cache_trim.restype = ctypes.c_int
+    lib.varlen_attn_cache_trim.argtypes = [vp, vp, vp, i32, vp]
+    lib.varlen_attn_cache_move.restype = ctypes.c_int
+    lib.varlen_attn_cache_move.argtypes = [vp, i32, vp, i32, i32, vp, i64, vp, i32, vp]
+    lib.varlen_attn_rotary_turns.restype = ctypes.c_int
+    lib.varlen_attn_rotary_turns.argtypes = [vp, i32, vp]
+    lib.varlen_attn_rotary.restype = ctypes.c_int
+    lib.varlen_attn_rotary.argtypes = [vp, S, vp, S, vp, vp, i32, i32, i32, i32, i32, vp, i32, vp, S, vp, S, vp]
+    lib.varlen_attn_rotary_cache_write.restype = ctypes.c_int
+    lib.varlen_attn_rotary_cache_write.argtypes = [vp, S, vp, S, vp, S, vp, vp, i32, i32, vp, vp, vp, S, vp]
     lib.varlen_attn_bwd_noalloc.restype = ctypes.c_int
     lib.varlen_attn_bwd_noalloc.argtypes = [vp, S, vp, S, vp, S, vp, S, vp, S, vp, vp, vp, i32, i32, i32, i32, i32,
                                             i32, i32, f32, vp, S, vp, S, vp, S, vp]
@@ -176,7 +208,10 @@ EXPORTED = ("varlen_attn_fwd", "varlen_attn_bwd_workspace_size", "varlen_attn_bw
             "varlen_attn_debug_noalloc_scratch", "varlen_attn_bounds_checked", "varlen_attn_debug_set_span_slack",
             "varlen_attn_debug_skip_load", "varlen_attn_debug_mma_cycles", "varlen_attn_fwd_fp8_window",
             "varlen_attn_fwd_fp8_dense_workspace_size", "varlen_attn_fwd_fp8_dense", "varlen_attn_cache_write",
-            "varlen_attn_cache_read", "varlen_attn_fwd_paged_workspace_size", "varlen_attn_fwd_paged")
+            "varlen_attn_cache_read", "varlen_attn_fwd_paged_workspace_size", "varlen_attn_fwd_paged",
+            "varlen_attn_fwd_paged_tree", "varlen_attn_cache_plan_workspace_size", "varlen_attn_cache_plan",
+            "varlen_attn_cache_trim", "varlen_attn_cache_move", "varlen_attn_rotary_turns", "varlen_attn_rotary",
+            "varlen_attn_rotary_cache_write")
 
 # Size of the fixed device array varlen_attn_bwd_noalloc uses as scratch, as
 # compiled into the library.
@@ -397,6 +432,59 @@ def varlen_attn_fwd_paged(q, cu_seqlens_q, batch, total_q, num_heads, max_seqlen
     return LIB.varlen_attn_fwd_paged(_ptr(q), _stride(q), _ptr(cu_seqlens_q), batch, total_q, num_heads,
                                      max_seqlen_q, _ref(cache), scale, window_left, window_right, _ptr(out),
                                      _stride(out), _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def varlen_attn_fwd_paged_tree(q, cu_seqlens_q, batch, total_q, num_heads, max_seqlen_q, cache, scale, masks, mask_words,
+                               positions, window_left, out, lse, workspace, workspace_bytes, stream=None) -> int:
+    return LIB.varlen_attn_fwd_paged_tree(_ptr(q), _stride(q), _ptr(cu_seqlens_q), batch, total_q, num_heads,
+                                          max_seqlen_q, _ref(cache), scale, _ptr(masks), mask_words, _ptr(positions),
+                                          window_left, _ptr(out), _stride(out), _ptr(lse), _ptr(workspace),
+                                          workspace_bytes, _stream(stream))
+
+
+def varlen_attn_cache_plan_workspace_size(batch) -> int:
+    return int(LIB.varlen_attn_cache_plan_workspace_size(batch))
+
+
+def varlen_attn_cache_plan(pool, new_lens, batch, parents, total, cu_seqlens, slots, positions, unplaced, masks,
+                           mask_words, workspace, workspace_bytes, stream=None) -> int:
+    """pool: a VarlenPagePool (PagePool.struct), or None."""
+    return LIB.varlen_attn_cache_plan(_ref(pool), _ptr(new_lens), batch, _ptr(parents), total, _ptr(cu_seqlens),
+                                      _ptr(slots), _ptr(positions), _ptr(unplaced), _ptr(masks), mask_words,
+                                      _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def varlen_attn_cache_trim(pool, lens, cu_seqlens, batch, stream=None) -> int:
+    return LIB.varlen_attn_cache_trim(_ref(pool), _ptr(lens), _ptr(cu_seqlens), batch, _stream(stream))
+
+
+def varlen_attn_cache_move(caches, cu_seqlens, batch, total, kept, kept_stride, kept_lens, max_kept, stream=None) -> int:
+    """caches: VarlenKvCache structs."""
+    arr = (VarlenKvCache * len(caches))(*caches)
+    return LIB.varlen_attn_cache_move(arr, len(caches), _ptr(cu_seqlens), batch, total, _ptr(kept), kept_stride,
+                                      _ptr(kept_lens), max_kept, _stream(stream))
+
+
+def varlen_attn_rotary_turns(frequencies):
+    """(status, turns): frequencies in radians a position as whole 2^-64 turns."""
+    n = len(frequencies)
+    turns = (ctypes.c_uint64 * max(n, 1))()
+    st = LIB.varlen_attn_rotary_turns((ctypes.c_double * max(n, 1))(*frequencies), n, turns)
+    return st, list(turns)[:n]
+
+
+def varlen_attn_rotary(q, k, positions, cu_seqlens, batch, total, num_heads, num_kv_heads, head_dim, rotary, inverse,
+                       q_out, k_out, stream=None) -> int:
+    """rotary: a VarlenRotary (Rotary.struct), or None."""
+    return LIB.varlen_attn_rotary(_ptr(q), _stride(q), _ptr(k), _stride(k), _ptr(positions), _ptr(cu_seqlens), batch,
+                                  total, num_heads, num_kv_heads, head_dim, _ref(rotary), int(bool(inverse)), _ptr(q_out),
+                                  _stride(q_out), _ptr(k_out), _stride(k_out), _stream(stream))
+
+
+def varlen_attn_rotary_cache_write(q, k, v, positions, slots, total, num_heads, cache, rotary, q_out, stream=None) -> int:
+    return LIB.varlen_attn_rotary_cache_write(_ptr(q), _stride(q), _ptr(k), _stride(k), _ptr(v), _stride(v),
+                                              _ptr(positions), _ptr(slots), total, num_heads, _ref(cache), _ref(rotary),
+                                              _ptr(q_out), _stride(q_out), _stream(stream))
 
 
 def varlen_attn_debug_noalloc_scratch():
@@ -683,7 +771,7 @@ def _cu(cache, cu):
 
 
 def _paged_call(entry, cache, stream, fresh, args):
-    """Runs a C entry point with the cache's device current.  Tensors that the
+    """Runs a C entry point with the cache's (or another handle's) device current.  Tensors that the
     call allocated (`fresh`) belong to the current stream: another `stream`
     waits for it (their memory may still be in use there), and they are kept
     from reuse until `stream` is done with them."""
@@ -776,3 +864,294 @@ def attention_fwd_paged(q, cache, cu_seqlens_q, max_seqlen_q=0, scale=None, out=
                 (qp, qs, cu, cache.batch, total_q, H, max_seqlen_q, cache.ref, D ** -0.5 if scale is None else scale,
                  left, right, op, os_, lse.data_ptr(), workspace.data_ptr(), nbytes))
     return out, lse
+
+
+def attention_fwd_paged_tree(q, cache, cu_seqlens_q, masks, max_seqlen_q=0, scale=None, window_left=-1, positions=None,
+                             out=None, lse=None, workspace=None, stream=None):
+    """O and LSE of packed queries over the cache, which already holds their own
+    rows: each sees the context and those new rows of its segment whose bit its
+    row of masks ([rows, words] int32, as StepPlan has them) has set.  With
+    window_left >= 0 the context is seen that far back from positions ([rows]
+    int32); everything else as in attention_fwd_paged."""
+    total_q, H, D = q.shape
+    qp, qs = _packed(cache, q, H)
+    cu = _cu(cache, cu_seqlens_q)
+    if masks.dtype not in (torch.int32, torch.uint32) or masks.dim() != 2 or masks.shape[0] != total_q \
+            or not masks.is_contiguous() or masks.device != cache.device:
+        raise ValueError("masks must be contiguous int32 [rows, words] on the cache's device")
+    pos = None if positions is None else _list(cache, positions, total_q, "positions", "rows")
+    fresh = []
+    if out is None:
+        out, op, os_ = _fresh_packed(cache, total_q, H)
+        fresh.append(out)
+    else:
+        op, os_ = _packed(cache, out, H, total_q)
+    if lse is None:
+        lse = torch.empty((H, total_q), dtype=torch.float32, device=cache.device)
+        fresh.append(lse)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (H, total_q) or not lse.is_contiguous() \
+            or lse.device != cache.device:
+        raise ValueError("lse must be contiguous float32 [H, rows] on the cache's device")
+    if workspace is None:
+        nbytes = _paged_workspace_bytes(cache.batch, total_q, H, cache.num_kv_heads, D)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+        fresh.append(workspace)
+    else:
+        if workspace.device != cache.device or not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous and on the cache's device")
+        nbytes = workspace.numel() * workspace.element_size()
+    _paged_call(LIB.varlen_attn_fwd_paged_tree, cache, stream, fresh,
+                (qp, qs, cu, cache.batch, total_q, H, max_seqlen_q, cache.ref, D ** -0.5 if scale is None else scale,
+                 masks.data_ptr(), masks.shape[1], pos, max(window_left, -1), op, os_, lse.data_ptr(),
+                 workspace.data_ptr(), nbytes))
+    return out, lse
+
+
+# ---------------------------------------------------------------- a step's lists
+
+def _list(owner, t, n, name, what, dtype=torch.int32):
+    """Address of a contiguous list of n entries on the owner's device."""
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError("%s must be contiguous %s [%s]" % (name, str(dtype)[6:], what))
+    if t.device != owner.device:
+        raise ValueError("every tensor must be on one device (%s is not)" % name)
+    return t.data_ptr()
+
+
+class _Fixed:
+    """A handle whose attributes are set once: calls go by addresses that another
+    tensor in the place of one would not change."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__ and self.__dict__[name] is not value:
+            raise AttributeError("%s.%s is fixed: write into the tensor, or make another %s"
+                                 % (type(self).__name__, name, type(self).__name__))
+        object.__setattr__(self, name, value)
+
+
+class PagePool(_Fixed):
+    """The pages of a cache as steps hand them out and take them back.
+
+    block_table     [batch, max_pages] int32, the table of the caches (all layers')
+    seqlens         [batch] int32: positions each sequence holds
+    free_pages      [num_pages] int32: a stack whose first free_count pages are free
+    free_count      [1] int32
+    seqlens_out, free_count_out   where the state after a call goes; None: in place
+
+    As PagedCache, it keeps the tensors themselves."""
+
+    def __init__(self, block_table, seqlens, free_pages, free_count, page_size, seqlens_out=None, free_count_out=None):
+        if block_table.dim() != 2 or block_table.dtype != torch.int32 or (block_table.shape[1] > 1
+                                                                          and block_table.stride(1) != 1):
+            raise ValueError("block_table must be int32 [batch, max_pages] with unit innermost stride")
+        self.device, self.batch = block_table.device, block_table.shape[0]
+        self.block_table, self.seqlens, self.free_pages, self.free_count = block_table, seqlens, free_pages, free_count
+        self.seqlens_out = seqlens if seqlens_out is None else seqlens_out
+        self.free_count_out = free_count if free_count_out is None else free_count_out
+        c = VarlenPagePool()
+        c.block_table, c.table_stride = block_table.data_ptr(), block_table.stride(0)
+        c.seqlens = _list(self, seqlens, self.batch, "seqlens", "batch")
+        c.seqlens_out = _list(self, self.seqlens_out, self.batch, "seqlens_out", "batch")
+        c.free_pages = _list(self, free_pages, free_pages.numel(), "free_pages", "num_pages")
+        c.free_count = _list(self, free_count, 1, "free_count", "1")
+        c.free_count_out = _list(self, self.free_count_out, 1, "free_count_out", "1")
+        c.num_pages, c.page_size, c.max_pages = free_pages.numel(), page_size, block_table.shape[1]
+        self.struct, self.ref = c, ctypes.byref(c)
+
+
+class StepPlan(_Fixed):
+    """What cache_plan writes for steps of up to `total` new rows of `batch`
+    sequences: cu_seqlens [batch + 1], positions [total], unplaced [batch] (int32),
+    slots [total] (int64) and, with mask_words > 0, masks [total, mask_words]
+    (int32).  Made once, filled by every step."""
+
+    def __init__(self, batch, total, device, mask_words=0):
+        def new(*shape, dtype=torch.int32):
+            return torch.zeros(shape, dtype=dtype, device=device)
+        self.batch, self.total, self.mask_words = batch, total, mask_words
+        self.cu_seqlens, self.positions, self.unplaced = new(batch + 1), new(total), new(batch)
+        self.slots = new(total, dtype=torch.int64)
+        self.masks = new(total, mask_words) if mask_words > 0 else None
+        nbytes = varlen_attn_cache_plan_workspace_size(batch)
+        self.workspace = new(max(nbytes, 16), dtype=torch.uint8)
+        self.device = self.slots.device
+        self.args = (self.cu_seqlens.data_ptr(), self.slots.data_ptr(), self.positions.data_ptr(), self.unplaced.data_ptr(),
+                     None if self.masks is None else self.masks.data_ptr(), mask_words, self.workspace.data_ptr(), nbytes)
+
+
+def cache_plan(pool, plan, new_lens, parents=None, stream=None):
+    """Fills `plan` for a step with new_lens[b] new rows of sequence b ([batch]
+    int32), takes the pages that they need from `pool` and advances its lengths.
+    parents ([total] int32, packed like the rows): the row of its own segment that
+    each one continues, negative for the context; then plan.masks and the rows'
+    depths in plan.positions follow the trees.  Returns plan."""
+    if plan.batch != pool.batch or plan.device != pool.device:
+        raise ValueError("the plan is not one for this pool's batch and device")
+    up = None
+    if parents is not None:
+        if plan.masks is None:
+            raise ValueError("trees need a plan with mask_words > 0")
+        up = _list(pool, parents, plan.total, "parents", "total")
+    _paged_call(LIB.varlen_attn_cache_plan, pool, stream, (),
+                (pool.ref, _list(pool, new_lens, pool.batch, "new_lens", "batch"), pool.batch, up, plan.total) + plan.args)
+    return plan
+
+
+def cache_trim(pool, lens, cu_seqlens=None, stream=None):
+    """Shortens sequence b to lens[b] positions or, with the cu_seqlens of a step,
+    to lens[b] of that step's rows, and puts the pages that this leaves empty back."""
+    _paged_call(LIB.varlen_attn_cache_trim, pool, stream, (),
+                (pool.ref, _list(pool, lens, pool.batch, "lens", "batch"),
+                 None if cu_seqlens is None else _list(pool, cu_seqlens, pool.batch + 1, "cu_seqlens", "batch + 1"),
+                 pool.batch))
+
+
+def cache_move(caches, cu_seqlens, kept, kept_lens, stream=None):
+    """In every cache of `caches` (layers over one table; or one cache) new row
+    kept[b, i] of sequence b becomes its new row i, i < kept_lens[b]; kept
+    [batch, most] int32, ascending in a row.  The caches' seqlens count all new
+    rows of cu_seqlens; cache_trim drops the others."""
+    if isinstance(caches, PagedCache):
+        caches = (caches,)
+    if len(caches) == 0:
+        return
+    first = caches[0]
+    for c in caches:
+        if c.device != first.device:
+            raise ValueError("the caches must be on one device")
+    ref = first.ref if len(caches) == 1 else (VarlenKvCache * len(caches))(*[c.struct for c in caches])
+    if kept.dtype != torch.int32 or kept.dim() != 2 or kept.shape[0] != first.batch or kept.device != first.device \
+            or (kept.shape[1] > 1 and kept.stride(1) != 1):
+        raise ValueError("kept must be int32 [batch, most] with unit innermost stride on the caches' device")
+    _paged_call(LIB.varlen_attn_cache_move, first, stream, (),
+                (ref, len(caches), _cu(first, cu_seqlens), first.batch, 0x7fffffff, kept.data_ptr(), kept.stride(0),
+                 _list(first, kept_lens, first.batch, "kept_lens", "batch"), kept.shape[1]))
+
+
+# ---------------------------------------------------------------- rotary positions
+
+def rotary_frequencies(rotary_dim, base=10000.0, stretch=1.0, how="ramp", trained=8192, low=1.0, high=32.0):
+    """(frequencies, scale): rotary_dim / 2 float64 radians a position, f_i =
+    base^(-2 i / rotary_dim), for contexts `stretch` times the `trained` ones, and
+    the factor on the turned elements that goes with it.  how:
+      "linear"  all frequencies / stretch;
+      "base"    a larger base, base * stretch^(rotary_dim / (rotary_dim - 2)), so
+                that the slowest pair is stretched whole and the fastest not at all;
+      "ramp"    pairs that turn at least `high` times within `trained` positions are
+                kept, those that turn at most `low` times are stretched, linear in
+                the number of turns between; scale 0.1 ln(stretch) + 1."""
+    if rotary_dim < 2 or rotary_dim % 2 or base <= 0 or stretch <= 0 or how not in ("linear", "base", "ramp"):
+        raise ValueError("rotary_dim must be even, base and stretch positive, how linear, base or ramp")
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+    if stretch == 1:
+        return base ** (-i / rotary_dim), 1.0
+    if how == "base":
+        wide = base * stretch ** (rotary_dim / (rotary_dim - 2)) if rotary_dim > 2 else base
+        return wide ** (-i / rotary_dim), 1.0
+    f = base ** (-i / rotary_dim)
+    if how == "linear":
+        return f / stretch, 1.0
+    keep = torch.clamp((f * trained / (2 * math.pi) - low) / (high - low), 0, 1)
+    return f * keep + f / stretch * (1 - keep), 0.1 * math.log(stretch) + 1
+
+
+class Rotary(_Fixed):
+    """Rotary positions: the frequencies (radians a position, one for each pair, any
+    sequence or tensor) as the kernels take them, how the pairs lie (interleaved:
+    2i and 2i + 1; else i and i + rotary_dim / 2) and the factor on what they give."""
+
+    def __init__(self, frequencies, interleaved=False, scale=1.0, device=None):
+        if isinstance(frequencies, torch.Tensor):
+            if device is None and frequencies.is_cuda:
+                device = frequencies.device
+            frequencies = frequencies.tolist()
+        st, turns = varlen_attn_rotary_turns([float(f) for f in frequencies])
+        _check(st, "varlen_attn_rotary_turns")
+        whole = [t - (1 << 64) if t >= 1 << 63 else t for t in turns]  # the same bits
+        self.turns = torch.tensor(whole, dtype=torch.int64, device="cuda" if device is None else device)
+        self.device, self.rotary_dim = self.turns.device, 2 * len(turns)
+        self.interleaved, self.scale = bool(interleaved), float(scale)
+        c = VarlenRotary()
+        c.turns, c.rotary_dim, c.interleaved, c.scale = self.turns.data_ptr(), 2 * len(turns), int(self.interleaved), self.scale
+        self.struct, self.ref = c, ctypes.byref(c)
+
+
+def _rows(owner, t, name, dim, total, heads=None):
+    """(heads, address, strides) of packed rows."""
+    n, h, d = t.shape
+    st = t.stride()
+    if t.dtype != torch.bfloat16 or n != total or d != dim or st[2] != 1 or (heads is not None and h != heads):
+        raise ValueError("%s must be bfloat16 [%d, %s, %d] with unit innermost stride"
+                         % (name, total, "heads" if heads is None else heads, dim))
+    if t.device != owner.device:
+        raise ValueError("every tensor must be on one device (%s is not)" % name)
+    return h, t.data_ptr(), VarlenStride(st[0], st[1])
+
+
+def _turned(owner, t, out, name, dim, total, fresh):
+    """Arguments of an input and of the output that it is turned into (allocated when None)."""
+    h, p, s = _rows(owner, t, name, dim, total)
+    if out is None:
+        out = torch.empty((total, h, dim), dtype=torch.bfloat16, device=owner.device)
+        fresh.append(out)
+        return out, h, p, s, out.data_ptr(), VarlenStride(h * dim, dim)
+    _, op, os_ = _rows(owner, out, name + "_out", dim, total, h)
+    return out, h, p, s, op, os_
+
+
+_NO_STRIDE = VarlenStride(0, 0)
+
+
+def _rotary(q, k, rope, positions, cu_seqlens, q_out, k_out, stream, inverse):
+    total, _, dim = q.shape
+    fresh = []
+    q_out, H, qp, qs, qop, qos = _turned(rope, q, q_out, "q", dim, total, fresh)
+    if k is None:
+        k_out, Hk, kp, ks, kop, kos = None, 0, None, _NO_STRIDE, None, _NO_STRIDE
+    else:
+        k_out, Hk, kp, ks, kop, kos = _turned(rope, k, k_out, "k", dim, total, fresh)
+    if positions is not None:
+        pos, cu, batch = _list(rope, positions, total, "positions", "rows"), None, 0
+    elif cu_seqlens is not None:
+        pos, batch = None, cu_seqlens.numel() - 1
+        cu = _list(rope, cu_seqlens, batch + 1, "cu_seqlens", "batch + 1")
+    else:
+        raise ValueError("rows need positions or cu_seqlens")
+    _paged_call(LIB.varlen_attn_rotary, rope, stream, fresh,
+                (qp, qs, kp, ks, pos, cu, batch, total, H, Hk, dim, rope.ref, inverse, qop, qos, kop, kos))
+    return q_out, k_out
+
+
+def rotary(q, k, rope, positions=None, cu_seqlens=None, q_out=None, k_out=None, stream=None):
+    """Packed rows q [rows, H, D] and k [rows, Hk, D] (bf16; k may be None) turned to
+    positions ([rows] int32) or, without them, to their places in the segments of
+    cu_seqlens; returns (q_out, k_out), allocated when None; an output may be its
+    own input.  Rows outside every segment are not written."""
+    return _rotary(q, k, rope, positions, cu_seqlens, q_out, k_out, stream, 0)
+
+
+def rotary_bwd(dq, dk, rope, positions=None, cu_seqlens=None, dq_out=None, dk_out=None, stream=None):
+    """The gradient of rotary: that with respect to its inputs from that with respect
+    to its outputs (turned back; the arguments are rotary's)."""
+    return _rotary(dq, dk, rope, positions, cu_seqlens, dq_out, dk_out, stream, 1)
+
+
+def rotary_cache_write(cache, q, k, v, rope, positions, slots, q_out=None, stream=None):
+    """A step's new rows on their way into the cache, in one kernel: q (or None)
+    turned and returned (q_out, allocated when None, may be q), k turned and
+    written with v to the places that slots ([rows] int64) name; positions and slots
+    as StepPlan has them."""
+    total, dim = k.shape[0], cache.head_dim
+    fresh = []
+    if q is None:
+        q_out, H, qp, qs, qop, qos = None, 0, None, _NO_STRIDE, None, _NO_STRIDE
+    else:
+        q_out, H, qp, qs, qop, qos = _turned(cache, q, q_out, "q", dim, total, fresh)
+    if rope.device != cache.device:
+        raise ValueError("the frequencies must be on the cache's device")
+    _, kp, ks = _rows(cache, k, "k", dim, total, cache.num_kv_heads)
+    _, vp, vs = _rows(cache, v, "v", dim, total, cache.num_kv_heads)
+    _paged_call(LIB.varlen_attn_rotary_cache_write, cache, stream, fresh,
+                (qp, qs, kp, ks, vp, vs, _list(cache, positions, total, "positions", "rows"),
+                 _list(cache, slots, total, "slots", "rows", torch.int64), total, H, cache.ref, rope.ref, qop, qos))
+    return q_out

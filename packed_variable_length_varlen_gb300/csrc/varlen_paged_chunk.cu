@@ -50,9 +50,6 @@ namespace varlen {
 
 namespace {
 
-template <bool TREE>
-using ChunkGeomOf = PagedGeom<kChunkRows, kChunkTile, true, TREE>;
-
 constexpr int kLeastTiles = 2;  // tiles per CTA when there are few
 constexpr int kPieces = 4;      // pieces that the producer may be ahead
 
@@ -103,13 +100,16 @@ struct PieceReader {
     ++n;
     return x.b >= 0;
   }
+  // The same for a reader that leaves the piece where it lies until it calls done().
+  __device__ __forceinline__ bool wait(ChunkShared& sh, volatile int* abort) {
+    const uint32_t i = n % kPieces, parity = (n / kPieces) & 1;
+    return mbar_wait_warp(&sh.piece_full[i], parity, abort) && sh.piece[i].b >= 0;
+  }
+  __device__ __forceinline__ void done(ChunkShared& sh) {
+    mbar_arrive(&sh.piece_empty[n % kPieces]);
+    ++n;
+  }
 };
-
-// any[k] without an array in memory.
-__device__ __forceinline__ uint32_t any_of(const uint32_t (&any)[4], int k) {
-  const uint32_t lo = (k & 1) ? any[1] : any[0], hi = (k & 1) ? any[3] : any[2];
-  return (k & 2) ? hi : lo;
-}
 
 __device__ __forceinline__ uint32_t mul_pair(uint32_t a, uint32_t b) {
   const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                               const __grid_constant__ CUtensorMap tm_vs, const PagedParams p, const PagedParts parts,
                               int32_t take) {
   using C = ChunkCfg<D, E4M3>;
-  using ChunkGeom = ChunkGeomOf<TREE>;
+  using ChunkGeom = PagedGeom<kChunkRows, kChunkTile, true, TREE>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_addr(smem) & 1023u) != 0) {
     paged_refuse(p, parts);
@@ -351,13 +351,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         const int32_t unit_lo = TREE ? tree_unit_lo(p, x) : x.u.lo;
         for (int32_t j = x.j0; j < tiles; ++j, pos += 2) {
           const uint32_t vpos = pos + 1, s = vpos % C::NSLOT;
-          if (!mbar_wait_warp(&sh.kv_full[s], (vpos / C::NSLOT) & 1, abort)) { ok = false; break; }
           const int32_t key0 = (x.u.tile0 + j) * kChunkTile;
+          const bool tail = TREE && key0 + kChunkTile > x.sk - x.n;  // has new rows
           const int lo = max(unit_lo - key0, 0), hi = min(x.u.hi - key0, kChunkTile);
+          uint32_t any[4] = {0, 0, 0, 0};
+          if (tail) tree_unit_bits(p, x, unit_lo, key0, any);
+          if (!mbar_wait_warp(&sh.kv_full[s], (vpos / C::NSLOT) & 1, abort)) { ok = false; break; }
           uint4* base = reinterpret_cast<uint4*>(ring + s * C::TILE);
-          if (TREE && key0 + kChunkTile > x.sk - x.n) {
-            uint32_t any[4];
-            tree_unit_bits(p, x, unit_lo, key0, any);
+          if (tail) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               for (int u = t; any[k] != ~0u && u < 32 * 8; u += 64)
@@ -387,27 +388,33 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
     const float c2 = p.scale_log2;
     const int32_t row_tok = row / p.group, row_head = row - row_tok * p.group;
     PieceReader<true> pieces;
-    PagedPiece x;
+    PagedPiece copy;
     uint32_t g = 0;
     bool ok = true;
-    while (ok && pieces.next(sh, x, abort)) {
+    while (ok && (TREE ? pieces.wait(sh, abort) : pieces.next(sh, copy, abort))) {
+      // (TREE needs a few registers more: what the piece says is read again where it is needed)
+      const PagedPiece& x = TREE ? sh.piece[pieces.n % kPieces] : copy;
       const int32_t tok = x.u.t0 + hf * half_tokens + row_tok;
       const bool live = row_tok < half_tokens && tok <= x.u.t1;
-      const int64_t orow = (int64_t)x.q0 + tok;
-      const int32_t head = x.kh * p.group + row_head;
       const int32_t tiles = min(x.j1, x.u.tiles) - x.j0;
-      if (hf == 1 && x.u.t1 - x.u.t0 < half_tokens) continue;  // no rows in this half
+      if (hf == 1 && x.u.t1 - x.u.t0 < half_tokens) {  // no rows in this half
+        if (TREE) pieces.done(sh);
+        continue;
+      }
       float m_use = -INFINITY, l = 0.f;
       // a row that is none sees all keys: what it computes goes nowhere, and its
       // warp is spared the selects
       int32_t key_lo = 0, key_hi = INT32_MAX;
+      const int32_t ctx = x.sk - x.n;
       if (live && TREE) {
-        key_lo = tree_lo(p, orow, x.sk - x.n);
+        key_lo = tree_lo(p, (int64_t)x.q0 + tok, ctx);
         key_hi = x.sk;
       } else if (live) {
         band_keys(tok, tok, x.n, x.sk, p.win_left, p.win_right, &key_lo, &key_hi);
       }
       const int32_t key0 = (x.u.tile0 + x.j0) * kChunkTile;
+      // TREE: the masks come near while the context's tiles are worked through
+      if (TREE && live && key0 + tiles * kChunkTile > ctx) tree_prefetch(p, (int64_t)x.q0 + tok);
       for (int32_t j = 0; j < tiles; ++j) {
         if (!mbar_wait_warp(&sh.s_full[hf], (g + j) & 1, abort)) { ok = false; break; }
         tc_fence_after();
@@ -429,13 +436,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(s[i]);
         // keys that the row does not see are set to -inf by select
         const int32_t lim = key_hi - (key0 + j * kChunkTile), lim_lo = key_lo - (key0 + j * kChunkTile);
-        if (TREE && key0 + (j + 1) * kChunkTile > x.sk - x.n) {
+        if (TREE) {
+          if (key0 + (j + 1) * kChunkTile > ctx || __any_sync(0xffffffffu, lim_lo > 0)) {  // new rows, or a window's edge
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int32_t rel = key0 + j * kChunkTile + 32 * k - (x.sk - x.n);
-            const uint32_t see = (live ? tree_bits(p, orow, rel) : ~0u) & bits_between(lim_lo - 32 * k, lim - 32 * k);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t see = live ? tree_bits(p, (int64_t)x.q0 + tok, key0 + j * kChunkTile + 32 * k - ctx) &
+                                              bits_between(lim_lo - 32 * k, lim - 32 * k) : ~0u;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[32 * k + i] = (see & (1u << i)) != 0 ? v[32 * k + i] : -INFINITY;
+              for (int i = 0; i < 32; ++i) v[32 * k + i] = (see & (1u << i)) != 0 ? v[32 * k + i] : -INFINITY;
+            }
           }
         } else if (__any_sync(0xffffffffu, lim_lo > 0)) {
 #pragma unroll
@@ -502,6 +511,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
       if (!ok) break;
       // epilogue: the last O += P V of this half, then O / l and LSE, or the partial result
       const bool whole = x.whole();
+      const int64_t orow = (int64_t)x.q0 + tok;
+      const int32_t head = x.kh * p.group + row_head;
       float* part = parts.o + ((2 * (int64_t)blockIdx.x + (x.begins() ? 1 : 0)) * parts.rows + hf * 128 + row) * D;
       if (tiles > 0) {
         if (!mbar_wait_warp(&sh.pv_done[hf], (g + tiles - 1) & 1, abort)) break;
@@ -545,6 +556,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
           *reinterpret_cast<float2*>(parts.ml + 2 * r) = make_float2(m_use, l);
       }
       tc_fence_before();
+      if (TREE) pieces.done(sh);
       g += tiles;
     }
   } else if constexpr (E4M3) {
@@ -557,10 +569,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
     const int cc = C::NC == 2 ? t >> 6 : 0, r0 = C::NC == 2 ? t & 63 : t;
     const int box_shift = min(p.pages.page_shift, 7);
     PieceReader<true> pieces;
-    PagedPiece x;
+    PagedPiece copy;
     uint32_t pos = 0;
     bool ok = true;
-    while (ok && pieces.next(sh, x, abort)) {
+    while (ok && (TREE ? pieces.wait(sh, abort) : pieces.next(sh, copy, abort))) {
+      const PagedPiece& x = TREE ? sh.piece[pieces.n % kPieces] : copy;  // (as the softmax)
       const int32_t tiles = min(x.j1, x.u.tiles);
       const int32_t unit_lo = TREE ? tree_unit_lo(p, x) : x.u.lo;
       for (int32_t j = x.j0; ok && j < tiles; ++j) {
@@ -576,14 +589,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
           uint8_t* dst = ring + s * C::TILE;
           // rows of V that no row of the unit sees may hold anything: cleared
           const int lo = which ? unit_lo - key0 : -1, hi = which ? x.u.hi - key0 : kChunkTile;
-          uint32_t any[4] = {~0u, ~0u, ~0u, ~0u};
-          if (TREE && which && key0 + kChunkTile > x.sk - x.n) tree_unit_bits(p, x, unit_lo, key0, any);
 #pragma unroll
           for (int i = 0; i < C::NC; ++i) {
             const int r = r0 + i * 64;
             const float f = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
                 sc + ((r >> box_shift) << 7) + ((r & ((1 << box_shift) - 1)) << 1)));
-            const bool keep = r >= lo && r < hi && (!TREE || ((any_of(any, r >> 5) >> (r & 31)) & 1u) != 0), large = keep && f > 0x1p7f;
+            const bool keep = r >= lo && r < hi, large = keep && f > 0x1p7f;
             // 2^120 * scale, 0 for a row to clear (the codes' bits are finite in any case)
             const float f1 = keep ? (large ? 0x1p127f : f * 0x1p120f) : 0.f;
             const uint32_t ff = pack_bf16x2(f1, f1);
@@ -615,11 +626,25 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
               }
             }
           }
+          if (TREE && which && key0 + kChunkTile > x.sk - x.n) {  // nor may new rows that no row of the unit sees
+            uint32_t any[4];
+            tree_unit_bits(p, x, unit_lo, key0, any);
+#pragma unroll
+            for (int i = 0; i < C::NC; ++i) {
+              const int r = r0 + i * 64, w = r >> 5;
+              const uint32_t lower = (w & 1) ? any[1] : any[0], upper = (w & 1) ? any[3] : any[2];
+              if ((((w & 2) ? upper : lower) >> (r & 31)) & 1u) continue;
+              uint4* to = reinterpret_cast<uint4*>(dst + cc * C::CHUNK + r * 128);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) to[k] = make_uint4(0, 0, 0, 0);
+            }
+          }
           fence_proxy_async_smem();
           mbar_arrive(&sh.kv_full[s]);
           mbar_arrive(&sh.raw_empty[rs]);
         }
       }
+      if (TREE && ok) pieces.done(sh);
     }
   }
 

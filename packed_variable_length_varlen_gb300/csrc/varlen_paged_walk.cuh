@@ -282,6 +282,13 @@ __device__ __forceinline__ uint32_t tree_word_at(const PagedParams& p, int64_t r
   return (uint32_t)w < (uint32_t)p.mask_words && in_span(p.masks_span, a, 4, p.err) ? *a : 0u;
 }
 
+// Brings the first 512 bytes of a row's mask as far as L1 (a hint: nothing waits for it).
+__device__ __forceinline__ void tree_prefetch(const PagedParams& p, int64_t row) {
+  const uint32_t* a = p.masks + row * p.mask_words;
+  for (int32_t w = 0; w < min(p.mask_words, 128); w += 32)
+    if (in_span(p.masks_span, a + w, 4, p.err)) asm volatile("prefetch.global.L1 [%0];" ::"l"(a + w));
+}
+
 // 32 bits of a packed row's mask, from new row `rel` on; those before new row 0
 // (the context's) are set.
 __device__ __forceinline__ uint32_t tree_bits(const PagedParams& p, int64_t row, int32_t rel) {

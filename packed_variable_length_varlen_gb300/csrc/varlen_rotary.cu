@@ -28,7 +28,9 @@ namespace varlen {
 namespace {
 
 constexpr int kRotaryThreads = 128;
-constexpr int kSweeps = 4;  // heads a lane takes
+constexpr int kWarps = kRotaryThreads / 32;
+constexpr int kPairs = 64;  // of a head, at most
+constexpr int kFewLanes = 1 << 17;  // lanes (one head each) up to which a lane takes one head
 
 // V bf16 elements.
 template <int V>
@@ -97,6 +99,31 @@ __device__ __forceinline__ void sincos_turn(uint32_t h, float& s, float& c) {
   c = ((q + 1) & 2) ? -b : b;
 }
 
+// The top 32 bits of pos * f mod 2^64.
+__device__ __forceinline__ uint32_t turns_of(int32_t pos, uint64_t f) {
+  const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32);
+  return (uint32_t)pos * hi + __umulhi((uint32_t)pos, lo) - (pos < 0 ? lo : 0u);
+}
+
+// N floats from shared memory; a is aligned to N of them or to 4 (N = 2: to 2).
+template <int N>
+__device__ __forceinline__ void get_floats(float* x, const float* a) {
+  if constexpr (N == 2) {
+    const float2 u = *reinterpret_cast<const float2*>(a);
+    x[0] = u.x;
+    x[1] = u.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 u = *reinterpret_cast<const float4*>(a + i);
+      x[i] = u.x;
+      x[i + 1] = u.y;
+      x[i + 2] = u.z;
+      x[i + 3] = u.w;
+    }
+  }
+}
+
 // (a, b) turned: c and s carry the scale.
 __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   const float y = fmaf(a, c, -b * s);
@@ -104,12 +131,15 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   a = y;
 }
 
-// LG: lanes of a head (a power of two >= head_dim / 2 V).
-template <int V, int LG, bool INTER, RotaryTo TO>
+// LG: lanes of a head (a power of two >= head_dim / 2 V); SWEEPS: heads that a lane takes.
+template <int V, int LG, bool INTER, RotaryTo TO, int SWEEPS>
 __global__ void __launch_bounds__(kRotaryThreads) varlen_rotary_kernel(const __grid_constant__ RotaryParams p) {
+  __shared__ __align__(16) float table[kWarps][2][kPairs];  // cosines and sines of a warp's row
   dependency_wait();
   dependents_may_launch();
-  constexpr int kSlots = 32 / LG, kBlock = kSlots * kSweeps;  // heads of a warp at once, and in all
+  constexpr int kSlots = 32 / LG, kBlock = kSlots * SWEEPS;  // heads of a warp at once, and in all
+  float* cosines = table[threadIdx.x >> 5][0];
+  float* sines = table[threadIdx.x >> 5][1];
   const int lane = threadIdx.x & 31, c = lane & (LG - 1), slot = lane / LG;
   const int32_t all = p.heads + (TO == kToRows ? 1 : 2) * p.kv_heads, blocks = (all + kBlock - 1) / kBlock;
   const int64_t units = (int64_t)p.total * blocks, step = (int64_t)gridDim.x * (kRotaryThreads / 32);
@@ -119,9 +149,9 @@ __global__ void __launch_bounds__(kRotaryThreads) varlen_rotary_kernel(const __g
   for (int64_t u = (int64_t)blockIdx.x * (kRotaryThreads / 32) + (threadIdx.x >> 5); u < units; u += step) {
     const int64_t row = u / blocks;
     const int32_t head0 = (int32_t)(u - row * blocks) * kBlock + slot;
-    Piece<V> lo[kSweeps], hi[kSweeps];
+    Piece<V> lo[SWEEPS], hi[SWEEPS];
 #pragma unroll
-    for (int i = 0; i < kSweeps; ++i) {
+    for (int i = 0; i < SWEEPS; ++i) {
       const int32_t h = head0 + i * kSlots, hk = h - p.heads, hv = hk - p.kv_heads;
       const __nv_bfloat16* a = nullptr;
       Span s = p.q_span;
@@ -153,16 +183,32 @@ __global__ void __launch_bounds__(kRotaryThreads) varlen_rotary_kernel(const __g
       here = row >= first && row < clamp_row(p.cu[b + 1], p.total);
     }
     if (!here) continue;  // warp-uniform
-    float cs[V], sn[V];
+    // the warp's lanes share the row's angles out
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      // pairs of this lane: V in a row, or (interleaved) V / 2 of each piece
-      const int i = INTER ? (at >> 1) + (j & (V / 2 - 1)) + (j >= V / 2 ? p.rot / 4 : 0) : at + j;
-      const uint64_t t = turns ? (uint64_t)(int64_t)pos * p.turns[i] : 0ull;
-      sincos_turn((uint32_t)(t >> 32), sn[j], cs[j]);
-      cs[j] *= p.scale;
-      sn[j] *= p.scale * p.sign;
+    for (int j = 0; j < kPairs; j += 32) {
+      const int i = j + lane;
+      if (i < p.rot / 2) {
+        float s, k;
+        sincos_turn(turns_of(pos, p.turns[i]), s, k);
+        cosines[i] = k * p.scale;
+        sines[i] = s * (p.scale * p.sign);
+      }
     }
+    __syncwarp();
+    float cs[V], sn[V];
+    if (turns) {  // pairs of this lane: V in a row, or (interleaved) V / 2 of each piece
+      constexpr int N = INTER ? V / 2 : V;
+#pragma unroll
+      for (int y = 0; y < V / N; ++y) {
+        const int first = INTER ? (at >> 1) + y * (p.rot / 4) : at;
+        get_floats<N>(&cs[y * N], cosines + first);
+        get_floats<N>(&sn[y * N], sines + first);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) cs[j] = sn[j] = 0.f;
+    }
+    __syncwarp();  // (the next row's angles take the same place)
     int32_t page = p.num_pages, in_page = 0;
     if (TO != kToRows) {
       const int64_t to = p.slots[row];
@@ -174,7 +220,7 @@ __global__ void __launch_bounds__(kRotaryThreads) varlen_rotary_kernel(const __g
       }
     }
 #pragma unroll
-    for (int i = 0; i < kSweeps; ++i) {
+    for (int i = 0; i < SWEEPS; ++i) {
       const int32_t h = head0 + i * kSlots, hk = h - p.heads, hv = hk - p.kv_heads;
       if (turns && hk < p.kv_heads) {
 #pragma unroll
@@ -239,13 +285,20 @@ __global__ void __launch_bounds__(kRotaryThreads) varlen_rotary_kernel(const __g
   }
 }
 
+template <int V, int LG, bool INTER, RotaryTo TO, int SWEEPS>
+cudaError_t launch_rotary_sweeps(const RotaryLaunch& L, cudaStream_t stream) {
+  constexpr int kBlock = 32 / LG * SWEEPS;
+  const int64_t all = L.p.heads + (int64_t)(TO == kToRows ? 1 : 2) * L.p.kv_heads;
+  const int64_t units = L.p.total * ((all + kBlock - 1) / kBlock);
+  const unsigned grid = (unsigned)std::min<int64_t>((units + kWarps - 1) / kWarps, 1 << 30);
+  return launch_overlapped(varlen_rotary_kernel<V, LG, INTER, TO, SWEEPS>, dim3(grid), kRotaryThreads, 0, stream, L.p);
+}
+
 template <int V, int LG, bool INTER, RotaryTo TO>
 cudaError_t launch_rotary_to(const RotaryLaunch& L, cudaStream_t stream) {
-  constexpr int kBlock = 32 / LG * kSweeps;
-  const int64_t all = L.p.heads + (int64_t)(TO == kToRows ? 1 : 2) * L.p.kv_heads;
-  const int64_t units = L.p.total * ((all + kBlock - 1) / kBlock), warps = kRotaryThreads / 32;
-  const unsigned grid = (unsigned)std::min<int64_t>((units + warps - 1) / warps, 1 << 30);
-  return launch_overlapped(varlen_rotary_kernel<V, LG, INTER, TO>, dim3(grid), kRotaryThreads, 0, stream, L.p);
+  const int64_t heads = (int64_t)L.p.total * (L.p.heads + (int64_t)(TO == kToRows ? 1 : 2) * L.p.kv_heads);
+  return heads * LG <= kFewLanes ? launch_rotary_sweeps<V, LG, INTER, TO, 1>(L, stream)
+                                 : launch_rotary_sweeps<V, LG, INTER, TO, 4>(L, stream);
 }
 
 template <int V, int LG>

@@ -742,6 +742,12 @@ class PagedCache:
         object.__setattr__(self, name, value)
 
 
+@functools.lru_cache(maxsize=1024)
+def _strides(row, head):
+    """A VarlenStride for the C entry points, which take it by value (making one costs as much as a launch's checks)."""
+    return VarlenStride(row, head)
+
+
 def _packed(cache, t, heads, rows=None):
     """(pointer, strides) of packed rows t, checked for what the C entry
     points cannot see: type, shape, place."""
@@ -752,14 +758,14 @@ def _packed(cache, t, heads, rows=None):
                          "heads of %d%s)" % (heads, cache.head_dim, "" if rows is None else ", %d rows" % rows))
     if t.device != cache.device:
         raise ValueError("every tensor must be on the cache's device")
-    return t.data_ptr(), VarlenStride(st[0], st[1])
+    return t.data_ptr(), _strides(st[0], st[1])
 
 
 def _fresh_packed(cache, rows, heads):
     """(tensor, pointer, strides) of new contiguous packed rows."""
     d = cache.head_dim
     t = torch.empty((rows, heads, d), dtype=torch.bfloat16, device=cache.device)
-    return t, t.data_ptr(), VarlenStride(heads * d, d)
+    return t, t.data_ptr(), _strides(heads * d, d)
 
 
 def _cu(cache, cu):
@@ -786,7 +792,7 @@ def _paged_call(entry, cache, stream, fresh, args):
         own.wait_stream(torch.cuda.current_stream(cache.device))
         for t in fresh:
             t.record_stream(own)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():  # (CUDA is set up: the handle's tensors are there)
         st = entry(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -1080,12 +1086,12 @@ def _rows(owner, t, name, dim, total, heads=None):
     """(heads, address, strides) of packed rows."""
     n, h, d = t.shape
     st = t.stride()
-    if t.dtype != torch.bfloat16 or n != total or d != dim or st[2] != 1 or (heads is not None and h != heads):
+    if n != total or d != dim or st[2] != 1 or t.dtype != torch.bfloat16 or (heads is not None and h != heads):
         raise ValueError("%s must be bfloat16 [%d, %s, %d] with unit innermost stride"
                          % (name, total, "heads" if heads is None else heads, dim))
     if t.device != owner.device:
         raise ValueError("every tensor must be on one device (%s is not)" % name)
-    return h, t.data_ptr(), VarlenStride(st[0], st[1])
+    return h, t.data_ptr(), _strides(st[0], st[1])
 
 
 def _turned(owner, t, out, name, dim, total, fresh):
@@ -1094,7 +1100,7 @@ def _turned(owner, t, out, name, dim, total, fresh):
     if out is None:
         out = torch.empty((total, h, dim), dtype=torch.bfloat16, device=owner.device)
         fresh.append(out)
-        return out, h, p, s, out.data_ptr(), VarlenStride(h * dim, dim)
+        return out, h, p, s, out.data_ptr(), _strides(h * dim, dim)
     _, op, os_ = _rows(owner, out, name + "_out", dim, total, h)
     return out, h, p, s, op, os_
 

@@ -5,8 +5,10 @@
 // Plan and trim write a few bytes a row and are bound by latency: one launch, two
 // or three prefix sums over the batch and a few dependent loads.  One CTA sums
 // up (rows, then pages needed, so that every sequence knows its first row and its
-// place on the stack of free pages), and small steps are finished by the same CTA.
-// Larger ones by a second kernel, a thread a row.  A row finds its page from its
+// place on the stack of free pages), and small steps without trees are finished by
+// the same CTA: 3.4 us for 512 rows, 4.3 for 2000, where a second kernel, a thread a
+// row, makes it 4.5 to 6.4 (for 262144 rows).  (Trees want all SMs even when small: one
+// CTA took 5.6 us for 2 trees of 32 rows and 8.6 for 62, two kernels take 5.2.)  A row finds its page from its
 // sequence's sums alone, so rows depend on nothing but those; the row that opens
 // a page writes the table's entry.
 //
@@ -25,7 +27,8 @@ namespace varlen {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;  // of the CTA that sums up
+constexpr int kPlanThreads = 1024;  // of the CTA that sums up; fewer sequences take fewer,
+constexpr int kPlanFew = 256;       // whose barriers cost less
 constexpr int kPlanSmall = 2048;    // rows up to which it does the rest as well
 constexpr int kRowThreads = 256;    // of the second kernel
 
@@ -37,7 +40,8 @@ __device__ __forceinline__ int64_t pages_of(const PoolView& c, int64_t len) {
   return (len + c.page_size - 1) >> c.page_shift;
 }
 
-// Inclusive sum over the CTA's kPlanThreads threads; `all` is the whole one.
+// Inclusive sum over the CTA's THREADS threads; `all` is the whole one.
+template <int THREADS>
 __device__ __forceinline__ long long block_inclusive(long long v, long long* sums, long long& all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
@@ -47,7 +51,7 @@ __device__ __forceinline__ long long block_inclusive(long long v, long long* sum
   }
   if (lane == 31) sums[warp] = v;
   __syncthreads();
-  long long s = sums[lane];
+  long long s = lane < THREADS / 32 ? sums[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long t = __shfl_up_sync(0xffffffffu, s, o);
@@ -193,36 +197,31 @@ __device__ __forceinline__ int32_t last_at_most(int32_t n, int64_t x, F first) {
 
 // ------------------------------------------------------------------ plan
 
-struct PlanSmall {
-  PlanSeq seq[kPlanThreads];
-  int32_t word0[kPlanThreads];  // first word of a sequence's rows, of the words of all
-  TreeNode node[kPlanSmall];
-};
-
-// Sums up; with `small`, which needs a batch of at most kPlanThreads and at most
-// kPlanSmall rows, does the rows as well.
-__global__ void __launch_bounds__(kPlanThreads) varlen_plan_kernel(const __grid_constant__ PlanParams p, int small) {
+// Sums up; with `small`, which needs a batch of at most THREADS and no trees, does the
+// rows as well.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) varlen_plan_kernel(const __grid_constant__ PlanParams p, int small) {
   __shared__ long long sums[32];
-  __shared__ PlanSmall sh;
+  __shared__ PlanSeq seqs[THREADS];
   dependency_wait();
   const PoolView& c = p.pool;
   const int32_t count = pool_free(c);
-  long long rows = 0, need_before = 0, words = 0;
+  long long rows = 0, need_before = 0;
   int32_t used = 0;  // pages that this thread's sequences bring the hand-out to
-  for (int32_t base = 0; base < p.batch; base += kPlanThreads) {
+  for (int32_t base = 0; base < p.batch; base += THREADS) {
     const int32_t b = base + threadIdx.x;
     const bool live = b < p.batch;
     const int32_t old = live ? pool_len(c, b) : 0;
     long long all;
     const long long want_rows = live ? max(p.new_lens[b], 0) : 0;
-    const long long end = rows + block_inclusive(want_rows, sums, all);
+    const long long end = rows + block_inclusive<THREADS>(want_rows, sums, all);
     rows += all;
     const int32_t r0 = (int32_t)min(end - want_rows, (long long)p.total), r1 = (int32_t)min(end, (long long)p.total);
     const int32_t n = r1 - r0;
     const int64_t have = pages_of(c, old), want = pages_of(c, (int64_t)old + n);
     const bool fits = want <= c.max_pages;
     const int64_t need = fits ? want - have : 0;
-    const long long upto = need_before + block_inclusive(need, sums, all);
+    const long long upto = need_before + block_inclusive<THREADS>(need, sums, all);
     need_before += all;
     const bool given = fits && (need == 0 || upto <= count);
     if (given && need > 0) used = max(used, (int32_t)upto);
@@ -233,54 +232,29 @@ __global__ void __launch_bounds__(kPlanThreads) varlen_plan_kernel(const __grid_
       c.seqlens_out[b] = (int32_t)min((int64_t)old + n, (int64_t)INT32_MAX);
       // (a sequence that needs no page has all its rows in pages of its own)
       p.unplaced[b] = given ? 0 : (int32_t)max((int64_t)old + n - max((int64_t)old, have << c.page_shift), (int64_t)0);
+      if (small) seqs[b] = s;
+      else p.seqs[b] = s;
+      if (p.parents != nullptr && n > 32 * p.mask_words) record_error(p.err, kErrBounds);
     }
-    if (small) {
-      sh.seq[threadIdx.x] = s;
-      if (p.parents != nullptr) {
-        const long long mine = (n + 31) / 32;
-        sh.word0[threadIdx.x] = (int32_t)(block_inclusive(mine, sums, words) - mine);
-      }
-    } else if (live) {
-      p.seqs[b] = s;
-    }
-    if (live && p.parents != nullptr && n > 32 * p.mask_words) record_error(p.err, kErrBounds);
   }
   dependents_may_launch();
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) used = max(used, __shfl_xor_sync(0xffffffffu, used, o));
-  __syncthreads();
   if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = used;
   __syncthreads();
   if (threadIdx.x < 32) {
-    used = (int32_t)sums[threadIdx.x];
+    used = threadIdx.x < THREADS / 32 ? (int32_t)sums[threadIdx.x] : 0;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) used = max(used, __shfl_xor_sync(0xffffffffu, used, o));
     if (threadIdx.x == 0) *c.free_count_out = count - used;
   }
   if (!small) return;
   const int32_t last = (int32_t)min(rows, (long long)p.total);
-  if (p.parents == nullptr) {
-    for (int32_t row = threadIdx.x; row < last; row += kPlanThreads) {
-      const int32_t b = last_at_most(p.batch, row, [&](int32_t i) { return sh.seq[i].row0; });
-      write_row(p, sh.seq[b], b, row - sh.seq[b].row0, 0);
-    }
-  } else {
-    const int lane = threadIdx.x & 31;
-    for (int32_t k = threadIdx.x >> 5; k < (int32_t)words; k += kPlanThreads / 32) {  // warp-uniform
-      const int32_t b = last_at_most(p.batch, k, [&](int32_t i) { return sh.word0[i]; });
-      const PlanSeq s = sh.seq[b];
-      const int32_t w = k - sh.word0[b], n = min(s.n, 32 * p.mask_words);
-      const TreeNode x = tree_word(p, s.row0, n, w);
-      if (32 * w + lane < n) sh.node[s.row0 + 32 * w + lane] = x;
-    }
-    __syncthreads();
-    for (int32_t k = threadIdx.x >> 5; k < (int32_t)words; k += kPlanThreads / 32) {
-      const int32_t b = last_at_most(p.batch, k, [&](int32_t i) { return sh.word0[i]; });
-      const PlanSeq s = sh.seq[b];
-      write_tree_rows(p, s, b, k - sh.word0[b], sh.node + s.row0, min(s.n, 32 * p.mask_words));
-    }
+  for (int32_t row = threadIdx.x; row < last; row += THREADS) {
+    const int32_t b = last_at_most(p.batch, row, [&](int32_t i) { return seqs[i].row0; });
+    write_row(p, seqs[b], b, row - seqs[b].row0, 0);
   }
-  for (int32_t row = last + threadIdx.x; row < p.total; row += kPlanThreads) write_padding(p, row);
+  for (int32_t row = last + threadIdx.x; row < p.total; row += THREADS) write_padding(p, row);
 }
 
 // A thread a row, without trees.
@@ -322,15 +296,16 @@ __global__ void __launch_bounds__(kRowThreads) varlen_plan_trees_kernel(const __
 
 // One CTA: the pages that come back, from the last sequence's last to the first's
 // first, form a list; entries that name a page are numbered and go onto the stack.
-__global__ void __launch_bounds__(kPlanThreads) varlen_trim_kernel(const __grid_constant__ TrimParams p) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) varlen_trim_kernel(const __grid_constant__ TrimParams p) {
   __shared__ long long sums[32];
-  __shared__ int32_t first[kPlanThreads], have[kPlanThreads];  // place in the list; pages before the call
+  __shared__ int32_t first[THREADS], have[THREADS];  // place in the list; pages before the call
   dependency_wait();
   dependents_may_launch();
   const PoolView& c = p.pool;
   const int32_t count = pool_free(c);
   long long pushed = 0;
-  for (int32_t base = 0; base < p.batch; base += kPlanThreads) {
+  for (int32_t base = 0; base < p.batch; base += THREADS) {
     const int32_t b = p.batch - 1 - base - (int32_t)threadIdx.x;
     const bool live = b >= 0;
     int64_t held = 0, keep = 0;
@@ -344,12 +319,12 @@ __global__ void __launch_bounds__(kPlanThreads) varlen_trim_kernel(const __grid_
       c.seqlens_out[b] = (int32_t)left;
     }
     long long all;
-    const long long end = block_inclusive(held - keep, sums, all);
+    const long long end = block_inclusive<THREADS>(held - keep, sums, all);
     first[threadIdx.x] = (int32_t)(end - (held - keep));  // (batch * max_pages < 2^31)
     have[threadIdx.x] = (int32_t)held;
     __syncthreads();
-    const int32_t live_n = min(p.batch - base, kPlanThreads);
-    for (long long f0 = 0; f0 < all; f0 += kPlanThreads) {  // CTA-uniform
+    const int32_t live_n = min(p.batch - base, THREADS);
+    for (long long f0 = 0; f0 < all; f0 += THREADS) {  // CTA-uniform
       const long long f = f0 + threadIdx.x;
       int32_t id = -1;
       if (f < all) {
@@ -362,7 +337,7 @@ __global__ void __launch_bounds__(kPlanThreads) varlen_trim_kernel(const __grid_
         }
       }
       long long kept;
-      const long long rank = block_inclusive(id >= 0 ? 1 : 0, sums, kept) - 1;
+      const long long rank = block_inclusive<THREADS>(id >= 0 ? 1 : 0, sums, kept) - 1;
       if (id >= 0) {
         const long long to = count + pushed + rank;
         if (to < c.num_pages) {
@@ -381,25 +356,95 @@ __global__ void __launch_bounds__(kPlanThreads) varlen_trim_kernel(const __grid_
 // ------------------------------------------------------------------ move
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 32;  // accepted rows looked up at once
-constexpr int kMoveBatch = 8;  // rows that a thread loads before it stores any
+constexpr int kMoveRows = 32;      // accepted rows looked up at once
+constexpr int kMoveLoads = 8;      // pieces of 16 bytes that a thread holds at once
+constexpr int kMovePieces = 1024;  // of a CTA
 
-// A CTA takes some heads of one sequence in one layer; a thread 16 bytes of the row
-// of one head of K or V (or its scale) through all accepted rows, in order: the place
-// of row i lies at or before its source, so what a thread has still to read it has
-// not yet overwritten, and no other thread touches its bytes.
+// Moves pieces t, t + kMoveThreads, ... (GROUPS of them at once) of the listed rows.
+// A thread takes a piece through all rows in order, kMoveLoads / GROUPS rows loaded
+// before any is stored: the place of row i lies at or before its source, so what a
+// thread has still to read it has not yet overwritten, and no other thread touches it.
+template <bool E4M3, int GROUPS>
+__device__ __forceinline__ void move_pieces(const MoveParams& p, const MoveLayer& layer, int32_t t, int32_t end,
+                                            int32_t rows, const int2* from, const int2* to) {
+  constexpr int ROWS = kMoveLoads / GROUPS;
+  const int32_t chunks = p.row_bytes / 16, items = 2 * chunks + (E4M3 ? 2 : 0);  // pieces of a head's rows
+  for (; t < end; t += GROUPS * kMoveThreads) {
+    uint8_t* base[GROUPS];
+    int64_t ps[GROUPS], rs[GROUPS];  // byte strides of pages and rows
+    Span s[GROUPS];
+    bool scale[GROUPS];
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      const int32_t at = min(t + g * kMoveThreads, end - 1), h = at / items, item = at - h * items;
+      scale[g] = E4M3 && item >= 2 * chunks;
+      const bool is_v = scale[g] ? item > 2 * chunks : item >= chunks;
+      if (scale[g]) {
+        uint8_t* a = reinterpret_cast<uint8_t*>(is_v ? layer.v_scale : layer.k_scale);
+        s[g] = Span{a, p.s_bytes};
+        base[g] = a + ((int64_t)h << (p.pages.page_shift + 1));
+        ps[g] = (int64_t)p.heads << (p.pages.page_shift + 1);
+        rs[g] = 2;
+      } else {
+        uint8_t* a = is_v ? layer.v : layer.k;
+        s[g] = Span{a, is_v ? p.vp_bytes : p.kp_bytes};
+        base[g] = a + h * (is_v ? p.v_head : p.k_head) + (item - (is_v ? chunks : 0)) * 16;
+        ps[g] = is_v ? p.v_page : p.k_page;
+        rs[g] = is_v ? p.v_row : p.k_row;
+      }
+    }
+    for (int32_t j0 = 0; j0 < rows; j0 += ROWS) {
+      uint4 x[GROUPS][ROWS];
+#pragma unroll
+      for (int e = 0; e < ROWS; ++e) {
+        const int2 f = from[min(j0 + e, rows - 1)];
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+          const uint8_t* a = base[g] + f.x * ps[g] + f.y * rs[g];
+          x[g][e] = make_uint4(0, 0, 0, 0);
+          if (scale[g]) {
+            if (in_span(s[g], a, 2, p.err)) x[g][e].x = *reinterpret_cast<const unsigned short*>(a);
+          } else {
+            if (in_span(s[g], a, 16, p.err)) x[g][e] = *reinterpret_cast<const uint4*>(a);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < ROWS; ++e) {
+        if (j0 + e >= rows) break;
+        const int2 f = to[j0 + e];
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+          if (t + g * kMoveThreads >= end) break;
+          uint8_t* a = base[g] + f.x * ps[g] + f.y * rs[g];
+          if (scale[g]) {
+            if (in_span(s[g], a, 2, p.err)) *reinterpret_cast<unsigned short*>(a) = (unsigned short)x[g][e].x;
+          } else {
+            if (in_span(s[g], a, 16, p.err)) *reinterpret_cast<uint4*>(a) = x[g][e];
+          }
+        }
+      }
+    }
+  }
+}
+
+// A CTA takes some of the pieces (16 bytes of a head's row of K or V, or its scale) of
+// one sequence's rows in one layer.  It looks up 32 accepted rows at a time and lists
+// those that do not stay.
 template <bool E4M3>
 __global__ void __launch_bounds__(kMoveThreads) varlen_move_kernel(const __grid_constant__ MoveParams p) {
-  __shared__ int32_t page_from[kMoveRows], row_from[kMoveRows], page_to[kMoveRows], row_to[kMoveRows];
+  __shared__ int2 from_at[kMoveRows], to_at[kMoveRows];  // (page, row in it)
+  __shared__ int32_t listed;
   dependency_wait();
   dependents_may_launch();
   const int32_t b = blockIdx.x;
   const MoveLayer& layer = p.layer[blockIdx.z];
+  // (an accepted row is read before it is known to be one: it lies within kept's rows)
+  int32_t k = threadIdx.x < min(kMoveRows, p.max_kept) ? p.kept[(int64_t)b * p.kept_stride + threadIdx.x] : 0;
   const int32_t r0 = clamp_row(p.cu[b], p.total), n = max(clamp_row(p.cu[b + 1], p.total) - r0, 0);
   const int32_t kept = min(max(p.kept_lens[b], 0), p.max_kept);
   const int64_t start = (int64_t)max(p.pages.seqlens[b], 0) - n;  // position of new row 0
-  const int32_t chunks = p.row_bytes / 16, items = 2 * chunks + (E4M3 ? 2 : 0);  // of a head
-  const int64_t all = (int64_t)p.heads * items;
+  const int32_t all = p.heads * (2 * (p.row_bytes / 16) + (E4M3 ? 2 : 0));  // (heads are bounded: no overflow)
   auto place = [&](int32_t i, int32_t& page, int32_t& row) {  // of new row i, or no page
     const int64_t at = start + i;
     page = p.pages.num_pages;
@@ -411,13 +456,12 @@ __global__ void __launch_bounds__(kMoveThreads) varlen_move_kernel(const __grid_
     }
     page = page_at(p.pages, b, (int32_t)(at >> p.pages.page_shift), p.err);
   };
-  for (int32_t i0 = 0; i0 < kept; i0 += kMoveRows) {
-    if (i0 > 0) __syncthreads();
-    if (threadIdx.x < kMoveRows) {
+  for (int32_t i0 = 0; i0 < kept; i0 += kMoveRows) {  // CTA-uniform
+    if (threadIdx.x < 32) {
       const int32_t i = i0 + threadIdx.x;
+      if (i0 > 0 && i < kept) k = p.kept[(int64_t)b * p.kept_stride + i];
       int32_t from = p.pages.num_pages, to = from, rf = 0, rt = 0;
       if (i < kept) {
-        const int32_t k = p.kept[(int64_t)b * p.kept_stride + i];
         if (k < i || k >= n) {
           record_error(p.err, kErrBounds);
         } else if (k != i) {
@@ -425,74 +469,34 @@ __global__ void __launch_bounds__(kMoveThreads) varlen_move_kernel(const __grid_
           place(i, to, rt);
         }
       }
-      const bool both = from < p.pages.num_pages && to < p.pages.num_pages;
-      page_from[threadIdx.x] = both ? from : -1;
-      row_from[threadIdx.x] = rf;
-      page_to[threadIdx.x] = to;
-      row_to[threadIdx.x] = rt;
+      const bool moves = from < p.pages.num_pages && to < p.pages.num_pages;
+      const unsigned who = __ballot_sync(0xffffffffu, moves);
+      if (moves) {
+        const int at = __popc(who & ((1u << threadIdx.x) - 1u));
+        from_at[at] = make_int2(from, rf);
+        to_at[at] = make_int2(to, rt);
+      }
+      if (threadIdx.x == 0) listed = __popc(who);
     }
     __syncthreads();
-    const int32_t rows = min(kept - i0, kMoveRows);
-    for (int64_t t = (int64_t)blockIdx.y * kMoveThreads + threadIdx.x; t < all; t += (int64_t)gridDim.y * kMoveThreads) {
-      const int32_t h = (int32_t)(t / items), item = (int32_t)(t - (int64_t)h * items);
-      if (!E4M3 || item < 2 * chunks) {
-        const bool is_v = item >= chunks;
-        uint8_t* base = (is_v ? layer.v : layer.k) + (int64_t)h * (is_v ? p.v_head : p.k_head) + (item - (is_v ? chunks : 0)) * 16;
-        const int64_t ps = is_v ? p.v_page : p.k_page, rs = is_v ? p.v_row : p.k_row;
-        const Span s{is_v ? layer.v : layer.k, is_v ? p.vp_bytes : p.kp_bytes};
-        for (int32_t j0 = 0; j0 < rows; j0 += kMoveBatch) {
-          uint4 x[kMoveBatch];
-#pragma unroll
-          for (int e = 0; e < kMoveBatch; ++e) {
-            const int32_t j = min(j0 + e, rows - 1);
-            x[e] = make_uint4(0, 0, 0, 0);
-            if (j0 + e < rows && page_from[j] >= 0) {
-              const uint8_t* a = base + page_from[j] * ps + row_from[j] * rs;
-              if (in_span(s, a, 16, p.err)) x[e] = *reinterpret_cast<const uint4*>(a);
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < kMoveBatch; ++e) {
-            const int32_t j = min(j0 + e, rows - 1);
-            if (j0 + e < rows && page_from[j] >= 0) {
-              uint8_t* a = base + page_to[j] * ps + row_to[j] * rs;
-              if (in_span(s, a, 16, p.err)) *reinterpret_cast<uint4*>(a) = x[e];
-            }
-          }
-        }
-      } else {
-        unsigned short* base = reinterpret_cast<unsigned short*>(item > 2 * chunks ? layer.v_scale : layer.k_scale);
-        const Span s{base, p.s_bytes};
-        for (int32_t j0 = 0; j0 < rows; j0 += kMoveBatch) {
-          unsigned short x[kMoveBatch];
-#pragma unroll
-          for (int e = 0; e < kMoveBatch; ++e) {
-            const int32_t j = min(j0 + e, rows - 1);
-            x[e] = 0;
-            if (j0 + e < rows && page_from[j] >= 0) {
-              const unsigned short* a = base + (((int64_t)page_from[j] * p.heads + h) << p.pages.page_shift) + row_from[j];
-              if (in_span(s, a, 2, p.err)) x[e] = *a;
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < kMoveBatch; ++e) {
-            const int32_t j = min(j0 + e, rows - 1);
-            if (j0 + e < rows && page_from[j] >= 0) {
-              unsigned short* a = base + (((int64_t)page_to[j] * p.heads + h) << p.pages.page_shift) + row_to[j];
-              if (in_span(s, a, 2, p.err)) *a = x[e];
-            }
-          }
-        }
-      }
+    const int32_t rows = listed;
+    for (int32_t w = blockIdx.y * kMovePieces; w < all && rows > 0; w += gridDim.y * kMovePieces) {
+      const int32_t t = w + (int32_t)threadIdx.x, end = min(w + kMovePieces, all);
+      if (rows <= 2) move_pieces<E4M3, 4>(p, layer, t, end, rows, from_at, to_at);
+      else if (rows <= 4) move_pieces<E4M3, 2>(p, layer, t, end, rows, from_at, to_at);
+      else move_pieces<E4M3, 1>(p, layer, t, end, rows, from_at, to_at);
     }
+    __syncthreads();  // the lists are read
   }
 }
 
 }  // namespace
 
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream) {
-  const bool small = p.batch <= kPlanThreads && p.total <= kPlanSmall;
-  cudaError_t e = launch_overlapped(varlen_plan_kernel, dim3(1), kPlanThreads, 0, stream, p, small ? 1 : 0);
+  const bool small = p.batch <= kPlanThreads && p.total <= kPlanSmall && p.parents == nullptr;
+  const bool few = p.batch <= kPlanFew && (!small || p.total <= kPlanFew);
+  const cudaError_t e = few ? launch_overlapped(varlen_plan_kernel<kPlanFew>, dim3(1), kPlanFew, 0, stream, p, small ? 1 : 0)
+                            : launch_overlapped(varlen_plan_kernel<kPlanThreads>, dim3(1), kPlanThreads, 0, stream, p, small ? 1 : 0);
   if (e != cudaSuccess || small || p.total == 0) return e;
   if (p.parents == nullptr) {
     const int64_t blocks = ((int64_t)p.total + kRowThreads - 1) / kRowThreads;
@@ -505,12 +509,13 @@ cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_trim(const TrimParams& p, cudaStream_t stream) {
-  return launch_overlapped(varlen_trim_kernel, dim3(1), kPlanThreads, 0, stream, p);
+  return p.batch <= kPlanFew ? launch_overlapped(varlen_trim_kernel<kPlanFew>, dim3(1), kPlanFew, 0, stream, p)
+                             : launch_overlapped(varlen_trim_kernel<kPlanThreads>, dim3(1), kPlanThreads, 0, stream, p);
 }
 
 cudaError_t launch_move(const MoveLaunch& L, cudaStream_t stream) {
   const int64_t items = (int64_t)L.p.heads * (2 * (L.p.row_bytes / 16) + (L.e4m3 ? 2 : 0));
-  const dim3 grid((unsigned)L.p.batch, (unsigned)std::min<int64_t>((items + kMoveThreads - 1) / kMoveThreads, 65535), (unsigned)L.layers);
+  const dim3 grid((unsigned)L.p.batch, (unsigned)std::min<int64_t>((items + kMovePieces - 1) / kMovePieces, 65535), (unsigned)L.layers);
   return L.e4m3 ? launch_overlapped(varlen_move_kernel<true>, grid, kMoveThreads, 0, stream, L.p)
                 : launch_overlapped(varlen_move_kernel<false>, grid, kMoveThreads, 0, stream, L.p);
 }

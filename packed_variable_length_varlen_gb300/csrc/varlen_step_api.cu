@@ -257,6 +257,7 @@ extern "C" int varlen_attn_cache_move(const varlen_kv_cache* caches, int32_t cou
         x.table_stride != c.table_stride || x.seqlens != c.seqlens || !same(x.sk, c.sk) || !same(x.sv, c.sv))
       return VARLEN_ERR_SHAPE;
   }
+  if (c.num_kv_heads > (1 << 20)) return VARLEN_ERR_SHAPE;
   if (cu_seqlens == nullptr || kept_lens == nullptr || (max_kept > 0 && kept == nullptr)) return VARLEN_ERR_NULL;
   if (kept_stride < 0) return VARLEN_ERR_STRIDE;
   int sms = 0;

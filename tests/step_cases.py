@@ -17,12 +17,14 @@ def ancestors(parents):
 
 def pack(rows, words):
     """Lists of bit numbers as 32-bit words (int32)."""
-    out = torch.zeros(len(rows), words, dtype=torch.int64)
-    for r, bits in enumerate(rows):
+    out = []
+    for bits in rows:
+        v = 0
         for i in bits:
-            if i < 32 * words:
-                out[r, i // 32] |= 1 << (i % 32)
-    return torch.where(out >= 1 << 31, out - (1 << 32), out).to(torch.int32)
+            v |= 1 << i
+        w = [(v >> (32 * k)) & 0xffffffff for k in range(words)]
+        out.append([x - (1 << 32) if x >> 31 else x for x in w])
+    return torch.tensor(out, dtype=torch.int32).reshape(len(rows), words)
 
 
 def random_tree(n, g, chain=0.3):

@@ -509,8 +509,9 @@ cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_trim(const TrimParams& p, cudaStream_t stream) {
-  return p.batch <= kPlanFew ? launch_overlapped(varlen_trim_kernel<kPlanFew>, dim3(1), kPlanFew, 0, stream, p)
-                             : launch_overlapped(varlen_trim_kernel<kPlanThreads>, dim3(1), kPlanThreads, 0, stream, p);
+  // (a few pages come back from each sequence)
+  return p.batch <= kPlanFew / 4 ? launch_overlapped(varlen_trim_kernel<kPlanFew>, dim3(1), kPlanFew, 0, stream, p)
+                                 : launch_overlapped(varlen_trim_kernel<kPlanThreads>, dim3(1), kPlanThreads, 0, stream, p);
 }
 
 cudaError_t launch_move(const MoveLaunch& L, cudaStream_t stream) {

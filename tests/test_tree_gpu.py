@@ -204,6 +204,64 @@ def _held(va, cache, n):
     return k.double(), v.double()
 
 
+# loads of CTA 0, K and V counted alike: 5000 keys are 79 tiles of 64 and 40 of 128, so CTA 0 has at least 2 tiles
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("which,new,columns", [(3, [3, 2], 1), (4, [100, 3], 1), (4, [70, 1], 1 << 14)])
+@pytest.mark.parametrize("load", [0, 3])
+def test_a_skipped_load_times_out_and_the_next_call_is_right(va, kind, which, new, columns, load):
+    """3: the kernel for few rows, 4: the one for many; the bounded waits run out, the call says so, the context lives on."""
+    assert va.varlen_attn_get_device_status() == 0
+    cache, _, _ = C.make_cache([5000, 900], 2, 128, 64, kind, DEV, columns=columns)
+    q = torch.randn(sum(new), 4, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    masks = torch.full((sum(new), 4), -1, dtype=torch.int32, device=DEV)
+    assert va.varlen_attn_debug_skip_load(which, load) == 0
+    try:
+        va.attention_fwd_paged_tree(q, cache, C.cu_of(new, DEV), masks, max_seqlen_q=max(new))
+        st = va.varlen_attn_get_device_status()
+    finally:
+        va.varlen_attn_debug_skip_load(which, -1)
+    assert st == va.VARLEN_ERR_TIMEOUT, va.varlen_attn_status_string(st)
+    _tree(va, new, [5000, 900], 4, 2, 128, 64, kind, columns=columns)
+
+
+def test_other_streams(va):
+    """On another stream than the current one: every operator's result is the same, memory that a call allocates included."""
+    kind, new, lens = "e4m3", [20, 3], [300, 77]
+    cache, _, _ = C.make_cache(lens, 2, 64, 16, kind, DEV)
+    q = torch.randn(23, 4, 64, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    k = q[:, :2].contiguous()
+    masks = torch.cat([S.pack(S.ancestors(S.random_tree(n, torch.Generator().manual_seed(n))), 1) for n in new]).to(DEV)
+    rope = va.Rotary(va.rotary_frequencies(64)[0], device=DEV)
+    pos, slots = _ints(list(range(23))), _ints(list(range(23)), torch.int64)
+    side = torch.cuda.Stream()
+
+    def all_of_it(stream):
+        torch.cuda._sleep(2000000)  # what the current stream still does with recycled memory
+        junk = [torch.full((23, 4, 64), 9.0, dtype=torch.bfloat16, device=DEV) for _ in range(4)]
+        del junk
+        a, b = va.rotary(q, k, rope, positions=pos, stream=stream)
+        c = va.rotary_cache_write(cache, q, k, k, rope, pos, slots, stream=stream)
+        out, lse = va.attention_fwd_paged_tree(c, cache, C.cu_of(new, DEV), masks, max_seqlen_q=20, stream=stream)
+        pool = va.PagePool(cache.block_table.clone(), _ints([5, 0]), torch.arange(30, dtype=torch.int32, device=DEV), _ints([30]), 16)
+        plan = va.StepPlan(2, 30, DEV, mask_words=1)
+        torch.cuda.synchronize()
+        va.cache_plan(pool, plan, _ints(new), parents=torch.full((30,), -1, dtype=torch.int32, device=DEV), stream=None)
+        torch.cuda.synchronize()
+        va.cache_move(cache, plan.cu_seqlens, _ints([[2, 5], [1, 2]]), _ints([2, 2]), stream=stream)
+        va.cache_trim(pool, _ints([1, 1]), plan.cu_seqlens, stream=stream)
+        torch.cuda.synchronize()
+        return [a, b, c, out, lse, pool.seqlens, pool.free_pages, pool.free_count, plan.slots, plan.masks, cache.k_pages.view(torch.uint8).clone()]
+
+    ref = all_of_it(None)
+    for stream in (side, side.cuda_stream):
+        cache2, _, _ = C.make_cache(lens, 2, 64, 16, kind, DEV)
+        for x, y in zip((cache.k_pages, cache.v_pages, cache.k_scale, cache.v_scale), (cache2.k_pages, cache2.v_pages, cache2.k_scale, cache2.v_scale)):
+            x.view(torch.uint8).copy_(y.view(torch.uint8))
+        for x, y in zip(all_of_it(stream), ref):
+            assert torch.equal(x, y)
+    _ok(va)
+
+
 # ------------------------------------------------------------------ a step, whole
 
 class _Model:

@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
           const uint32_t vpos = pos + 1, s = vpos % C::NSLOT;
           const int32_t key0 = (x.u.tile0 + j) * kChunkTile;
           const bool tail = TREE && key0 + kChunkTile > x.sk - x.n;  // has new rows
-          const int lo = max(unit_lo - key0, 0), hi = min(x.u.hi - key0, kChunkTile);
+          const int lo = min(max(unit_lo - key0, 0), kChunkTile), hi = min(x.u.hi - key0, kChunkTile);
           uint32_t any[4] = {0, 0, 0, 0};
           if (tail) tree_unit_bits(p, x, unit_lo, key0, any);
           if (!mbar_wait_warp(&sh.kv_full[s], (vpos / C::NSLOT) & 1, abort)) { ok = false; break; }

@@ -149,14 +149,16 @@ def test_rows_that_nobody_sees(va, kind, new, lens, heads):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
-@pytest.mark.parametrize("heads", [2, 40])
-def test_context_behind_every_window(va, kind, heads):
-    """Positions past the context by more than the window: keys at the unit's start that no row sees hold NaN."""
+@pytest.mark.parametrize("heads", [2, 7, 40])
+@pytest.mark.parametrize("left,shift", [(100, 60), (300, 290), (390, 200), (391, 390), (50, 70)])
+def test_context_behind_every_window(va, kind, heads, left, shift):
+    """Positions past the context: keys at the unit's start that no row sees, whole tiles of them too, hold NaN."""
     new, lens = [9], [400]
     cache, k, v = C.make_cache(lens, 1, 128, 16, kind, DEV)
-    left, shift, c = 100, 60, 391  # rows see [c + 60 - 100, c)
+    c = 391  # rows see [c + shift - left, c)
+    shown = min(shift, left)
     table = cache.block_table[0].tolist()
-    for at in range(c - left, c + shift - left):
+    for at in range(c - left, c + shown - left):
         pg, r = table[at // 16], at % 16
         if kind == "bf16":
             cache.k_pages[pg, r], cache.v_pages[pg, r] = math.nan, math.nan
@@ -169,7 +171,7 @@ def test_context_behind_every_window(va, kind, heads):
                                            positions=_ints([c + shift] * 9))
     _ok(va)
     seen = torch.zeros(9, 400, dtype=torch.bool, device=DEV)
-    seen[:, c + shift - left:c] = True
+    seen[:, c + shown - left:c] = True
     seen[torch.arange(9), c + torch.arange(9)] = True
     C.check_attend(out, lse, S.attend_tree(q, k[0], v[0], float(torch.tensor(128 ** -0.5)), seen), 128, 400)
 

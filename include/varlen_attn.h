@@ -475,7 +475,8 @@ int varlen_attn_fwd_paged_tree(const void* q, varlen_stride sq, const int32_t* c
  * ceil(seqlens[b] / page_size) table entries, no other sequence does (pages that
  * sequences share must not come back through varlen_attn_cache_trim), and the
  * entries behind them mean nothing.  The _out arrays receive the state after the
- * call; each may be the array it follows or another one.
+ * call; each may be the array it follows or another one (the caches of a step
+ * name the array that has its lengths after the plan).
  */
 typedef struct {
   int32_t* block_table;      /* [batch] rows of max_pages entries */
@@ -555,8 +556,8 @@ int varlen_attn_cache_trim(const varlen_page_pool* pool, const int32_t* lens, co
  * negative are passed over.  seqlens counts all n_b rows, before and after: the
  * rest goes with varlen_attn_cache_trim.  `caches` is a host array of `count`
  * caches (layers; at most 1024) of one shape, type and strides over one table and
- * one seqlens (VARLEN_ERR_SHAPE otherwise); sequences that move rows must not
- * share the pages of their new rows.  total bounds cu_seqlens as in
+ * one seqlens (VARLEN_ERR_SHAPE otherwise), none of them twice; sequences that
+ * move rows must not share the pages of their new rows.  total bounds cu_seqlens as in
  * varlen_attn_cache_write.
  */
 int varlen_attn_cache_move(const varlen_kv_cache* caches, int32_t count, const int32_t* cu_seqlens, int32_t batch,

@@ -279,11 +279,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
           }
           mma_commit(&sh.s_full[hf]);
         };
-        // O += P V over the 16-row steps of the keys below `nk`
+        // O += P V over the 16-row steps of the keys below `nk` (TREE: over all of them, as
+        // only a unit's last tile has others, whose P is 0 and whose rows of V are clear: a
+        // branch before each product costs 3 to 7% of the whole)
         auto issue_pv = [&](int hf, uint32_t slot, bool first, int nk) {
 #pragma unroll
           for (int kk = 0; kk < kChunkTile / 16; ++kk)
-            if (kk < nk)
+            if (TREE || kk < nk)
               mma_ts_lo(tmem + C::O_COL + hf * 128, tmem + hf * 128 + kk * 8, rV + ((slot * C::TILE + kk * 2048) >> 4),
                         kIdescO, (!first || kk > 0) ? 1u : 0u);
           mma_commit(&sh.pv_done[hf]);

@@ -430,7 +430,9 @@ __device__ __forceinline__ void move_pieces(const MoveParams& p, const MoveLayer
 
 // A CTA takes some of the pieces (16 bytes of a head's row of K or V, or its scale) of
 // one sequence's rows in one layer.  It looks up 32 accepted rows at a time and lists
-// those that do not stay.
+// those that do not stay.  Bound by the memory where there is much to move: 732 rows of
+// 56 heads of 128 in four bf16 layers, 168 MB, 31 us, 5.4 TB/s (a piece a thread 38.8;
+// 512 or 2048 pieces a CTA 34); else by four dependent loads: 214 rows of 8 E4M3 heads 3.6 us.
 template <bool E4M3>
 __global__ void __launch_bounds__(kMoveThreads) varlen_move_kernel(const __grid_constant__ MoveParams p) {
   __shared__ int2 from_at[kMoveRows], to_at[kMoveRows];  // (page, row in it)

@@ -14,8 +14,11 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import math
 import os
+import warnings
 
 import torch
 
@@ -194,8 +197,27 @@ def _load() -> ctypes.CDLL:
     return lib
 
 
+def _load_binding(lib):
+    """The native binding (csrc/varlen_binding.cpp) over the library's functions, or None: then every call goes by
+    ctypes, with the same results."""
+    if not _build.binding_built():
+        return None
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_varlen_binding", _build.BINDING)
+        native = importlib.util.module_from_spec(importlib.util.spec_from_loader("_varlen_binding", loader))
+        loader.exec_module(native)
+    except ImportError as e:
+        warnings.warn("small calls go by ctypes: %s cannot be loaded (%s)" % (_build.BINDING, e))
+        return None
+    native.bind(*(ctypes.cast(getattr(lib, "varlen_attn_" + name), ctypes.c_void_p).value
+                  for name in ("rotary", "rotary_cache_write", "cache_plan", "cache_trim", "cache_move", "fwd_paged_tree",
+                               "fwd_paged_workspace_size")))
+    return native
+
+
 LIB = _load()
 LIB_PATH = LIB._name
+NATIVE = _load_binding(LIB)
 
 EXPORTED = ("varlen_attn_fwd", "varlen_attn_bwd_workspace_size", "varlen_attn_bwd",
             "varlen_attn_get_device_status", "varlen_attn_status_string", "varlen_attn_tile_count",
@@ -732,7 +754,7 @@ class PagedCache:
         c.type = VARLEN_CACHE_E4M3 if e4m3 else VARLEN_CACHE_BF16
         c.num_pages, c.page_size, c.num_kv_heads, c.head_dim = pages, page_size, heads, dim
         c.max_pages = block_table.shape[1]
-        self.struct, self.ref = c, ctypes.byref(c)
+        self.struct, self.ref, self.at = c, ctypes.byref(c), _at(c, self.device)
 
     def __setattr__(self, name, value):
         # set once: calls use the struct, which another value here would not reach (the same tensor again is what
@@ -799,6 +821,18 @@ def _paged_call(entry, cache, stream, fresh, args):
             st = entry(*args, handle)
     if st != VARLEN_OK:
         raise VarlenError(st, entry.__name__)
+
+
+def _at(struct, device):
+    """A handle as the native binding takes it: its C description's address and its device's index (-1: none)."""
+    return ctypes.addressof(struct), -1 if device.index is None else device.index
+
+
+def _native(got, entry):
+    """What the native binding answered, a status other than VARLEN_OK raised as _paged_call does."""
+    if type(got) is int and got != VARLEN_OK:
+        raise VarlenError(got, entry)
+    return got
 
 
 def cache_write(cache, k, v, cu_seqlens, stream=None):
@@ -879,6 +913,11 @@ def attention_fwd_paged_tree(q, cache, cu_seqlens_q, masks, max_seqlen_q=0, scal
     row of masks ([rows, words] int32, as StepPlan has them) has set.  With
     window_left >= 0 the context is seen that far back from positions ([rows]
     int32); everything else as in attention_fwd_paged."""
+    if NATIVE is not None and stream is None and out is None and lse is None and workspace is None:
+        got = NATIVE.attention_fwd_paged_tree(cache.at, cache.batch, q, cu_seqlens_q, masks, max_seqlen_q, scale, window_left,
+                                              positions)
+        if got is not NotImplemented:
+            return _native(got, "varlen_attn_fwd_paged_tree")
     total_q, H, D = q.shape
     qp, qs = _packed(cache, q, H)
     cu = _cu(cache, cu_seqlens_q)
@@ -962,7 +1001,7 @@ class PagePool(_Fixed):
         c.free_count = _list(self, free_count, 1, "free_count", "1")
         c.free_count_out = _list(self, self.free_count_out, 1, "free_count_out", "1")
         c.num_pages, c.page_size, c.max_pages = free_pages.numel(), page_size, block_table.shape[1]
-        self.struct, self.ref = c, ctypes.byref(c)
+        self.struct, self.ref, self.at = c, ctypes.byref(c), _at(c, self.device)
 
 
 class StepPlan(_Fixed):
@@ -993,10 +1032,15 @@ def cache_plan(pool, plan, new_lens, parents=None, stream=None):
     depths in plan.positions follow the trees.  Returns plan."""
     if plan.batch != pool.batch or plan.device != pool.device:
         raise ValueError("the plan is not one for this pool's batch and device")
+    if parents is not None and plan.masks is None:
+        raise ValueError("trees need a plan with mask_words > 0")
+    if NATIVE is not None and stream is None:
+        got = NATIVE.cache_plan(pool.at, pool.batch, new_lens, parents, plan.total, plan.args)
+        if got is not NotImplemented:
+            _native(got, "varlen_attn_cache_plan")
+            return plan
     up = None
     if parents is not None:
-        if plan.masks is None:
-            raise ValueError("trees need a plan with mask_words > 0")
         up = _list(pool, parents, plan.total, "parents", "total")
     _paged_call(LIB.varlen_attn_cache_plan, pool, stream, (),
                 (pool.ref, _list(pool, new_lens, pool.batch, "new_lens", "batch"), pool.batch, up, plan.total) + plan.args)
@@ -1006,6 +1050,11 @@ def cache_plan(pool, plan, new_lens, parents=None, stream=None):
 def cache_trim(pool, lens, cu_seqlens=None, stream=None):
     """Shortens sequence b to lens[b] positions or, with the cu_seqlens of a step,
     to lens[b] of that step's rows, and puts the pages that this leaves empty back."""
+    if NATIVE is not None and stream is None:
+        got = NATIVE.cache_trim(pool.at, pool.batch, lens, cu_seqlens)
+        if got is not NotImplemented:
+            _native(got, "varlen_attn_cache_trim")
+            return
     _paged_call(LIB.varlen_attn_cache_trim, pool, stream, (),
                 (pool.ref, _list(pool, lens, pool.batch, "lens", "batch"),
                  None if cu_seqlens is None else _list(pool, cu_seqlens, pool.batch + 1, "cu_seqlens", "batch + 1"),
@@ -1022,6 +1071,11 @@ def cache_move(caches, cu_seqlens, kept, kept_lens, stream=None):
     if len(caches) == 0:
         return
     first = caches[0]
+    if NATIVE is not None and stream is None:
+        got = NATIVE.cache_move([c.at for c in caches], first.batch, cu_seqlens, kept, kept_lens)
+        if got is not NotImplemented:
+            _native(got, "varlen_attn_cache_move")
+            return
     for c in caches:
         if c.device != first.device:
             raise ValueError("the caches must be on one device")
@@ -1079,7 +1133,7 @@ class Rotary(_Fixed):
         self.interleaved, self.scale = bool(interleaved), float(scale)
         c = VarlenRotary()
         c.turns, c.rotary_dim, c.interleaved, c.scale = self.turns.data_ptr(), 2 * len(turns), int(self.interleaved), self.scale
-        self.struct, self.ref = c, ctypes.byref(c)
+        self.struct, self.ref, self.at = c, ctypes.byref(c), _at(c, self.device)
 
 
 def _rows(owner, t, name, dim, total, heads=None):
@@ -1109,6 +1163,10 @@ _NO_STRIDE = VarlenStride(0, 0)
 
 
 def _rotary(q, k, rope, positions, cu_seqlens, q_out, k_out, stream, inverse):
+    if NATIVE is not None and stream is None:
+        got = NATIVE.rotary(rope.at, inverse, q, k, positions, cu_seqlens, q_out, k_out)
+        if got is not NotImplemented:
+            return _native(got, "varlen_attn_rotary")
     total, _, dim = q.shape
     fresh = []
     q_out, H, qp, qs, qop, qos = _turned(rope, q, q_out, "q", dim, total, fresh)
@@ -1147,6 +1205,10 @@ def rotary_cache_write(cache, q, k, v, rope, positions, slots, q_out=None, strea
     turned and returned (q_out, allocated when None, may be q), k turned and
     written with v to the places that slots ([rows] int64) name; positions and slots
     as StepPlan has them."""
+    if NATIVE is not None and stream is None:
+        got = NATIVE.rotary_cache_write(cache.at, q, k, v, rope.at, positions, slots, q_out)
+        if got is not NotImplemented:
+            return _native(got, "varlen_attn_rotary_cache_write")
     total, dim = k.shape[0], cache.head_dim
     fresh = []
     if q is None:

@@ -28,7 +28,7 @@
 // TREE, drafted trees: in the tiles that hold new rows each score is looked up in its
 // row's mask, and a ballot over the lanes' answers says which rows of V some row of the
 // warp's row tile sees; the others are cleared (64 trees of 4 rows of 4 heads over 8192
-// E4M3 keys 286 us, as one token's 16 rows).
+// E4M3 keys 286 us).
 //
 // A CTA is four consumer warps and a producer warp; two (bf16) or three (E4M3)
 // CTAs share an SM.

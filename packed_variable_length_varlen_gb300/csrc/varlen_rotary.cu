@@ -20,7 +20,7 @@
 // below 2^-29 and 2^-31) are good to fp32's last bit.
 //
 // Measured: 262144 rows of 40 heads of 128, 629 us, 7.2 TB/s (a plain copy moves 6.8);
-// 29012 rows of 32 heads of 96, half of each turned, 58 us, 6.4 TB/s; 5984 rows of 32 heads,
+// 29012 rows of 32 heads of 96, half of each turned, 58 us, 6.4 TB/s; 7493 rows of 32 heads,
 // with 8 of K and of V into a bf16 cache, 32 us, 5.8 TB/s; 16 rows of those into an E4M3
 // cache 2.4 us, the launch and two memory latencies.  With angles worked out by every
 // lane the first was 667.

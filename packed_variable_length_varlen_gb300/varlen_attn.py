@@ -947,7 +947,7 @@ def attention_fwd_paged_tree(q, cache, cu_seqlens_q, masks, max_seqlen_q=0, scal
         nbytes = workspace.numel() * workspace.element_size()
     _paged_call(LIB.varlen_attn_fwd_paged_tree, cache, stream, fresh,
                 (qp, qs, cu, cache.batch, total_q, H, max_seqlen_q, cache.ref, D ** -0.5 if scale is None else scale,
-                 masks.data_ptr(), masks.shape[1], pos, max(window_left, -1), op, os_, lse.data_ptr(),
+                 masks.data_ptr(), masks.shape[1], pos, min(max(window_left, -1), 0x7fffffff), op, os_, lse.data_ptr(),
                  workspace.data_ptr(), nbytes))
     return out, lse
 
@@ -1011,6 +1011,9 @@ class StepPlan(_Fixed):
     (int32).  Made once, filled by every step."""
 
     def __init__(self, batch, total, device, mask_words=0):
+        if not (0 <= batch < 1 << 31 and 0 <= total < 1 << 31 and 0 <= mask_words < 1 << 31):
+            raise ValueError("batch, total and mask_words are numbers of 31 bits")
+
         def new(*shape, dtype=torch.int32):
             return torch.zeros(shape, dtype=dtype, device=device)
         self.batch, self.total, self.mask_words = batch, total, mask_words

@@ -51,3 +51,11 @@ def test_a_binding_of_another_torch_is_not_loaded(va, monkeypatch):
     monkeypatch.setattr(build, "binding_tag", lambda: "another")
     assert not build.binding_built()
     assert va._load_binding(va.LIB) is None
+
+
+def test_plans_past_32_bits(va):
+    for args in ((3, 1 << 31), (1 << 31, 3), (-1, 3), (3, -1)):
+        with pytest.raises(ValueError):
+            va.StepPlan(*args, "cpu")
+    with pytest.raises(ValueError):
+        va.StepPlan(3, 3, "cpu", mask_words=1 << 31)

@@ -237,3 +237,16 @@ def test_refusals_are_the_same(va, monkeypatch):
     assert kinds >= {ValueError, va.VarlenError}
     torch.cuda.synchronize()
     assert va.varlen_attn_get_device_status() == 0
+
+
+def test_windows_past_32_bits(va, monkeypatch):
+    s = _step(va)
+    n = sum(s["new"])
+    want = va.attention_fwd_paged_tree(s["q"], s["cache"], s["cu"], s["masks"])
+    for how in (va.NATIVE, None):
+        monkeypatch.setattr(va, "NATIVE", how)
+        for left in ((1 << 31) - 1, 1 << 31, (1 << 32) + 5, 1 << 80):
+            got = va.attention_fwd_paged_tree(s["q"], s["cache"], s["cu"], s["masks"], window_left=left, positions=s["pos"])
+            assert torch.equal(got[0][:n], want[0][:n]) and torch.equal(got[1][:, :n], want[1][:, :n])
+    torch.cuda.synchronize()
+    assert va.varlen_attn_get_device_status() == 0

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
     bool ok = true;
     walk.init(sh.start, p, take);
     while (ok && walk.next(p, x)) {
-      if (lane == 0) paged_note(p, parts, sh.start, x);
+      if (lane == 0) paged_note(p, parts, sh.start, walk, x);
       const int32_t tiles = min(x.j1, x.u.tiles);
       for (int32_t j = x.j0; ok && j < tiles; ++j) {
         const int32_t key = (x.u.tile0 + j) * C::KT + (piece << box_shift);

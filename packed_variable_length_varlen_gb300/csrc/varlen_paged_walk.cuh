@@ -6,9 +6,11 @@
 // group, head r % group.  A unit works through the key tiles that some of its
 // rows see.  The units of a launch in a fixed order (segment, key head, row
 // block), each with its tiles (at least one, so that a unit without keys is
-// visited and writes its zeros), form one long list of T tiles, and each of N
-// CTAs takes T / N neighbouring ones of it (the first T % N one more): every CTA
-// has the same number of tiles, whatever the lengths.  A CTA's part starts and ends inside a unit
+// visited and writes its zeros), form one long list of T places, and each of N
+// CTAs takes T / N neighbouring ones of it (the first T % N one more): the tiles
+// whose first place these are.  A tile has one place, so that every CTA has the same
+// number of them, whatever the lengths; with trees, whose units are many and short, more, by
+// what it costs, and so has the end of a unit.  A CTA's part starts and ends inside a unit
 // in general; what it has of a unit that it does not hold whole goes to the
 // workspace as a partial result (its running maximum, sum and unnormalised
 // output), in one of two slots: 1 for the unit that it begins and a later CTA
@@ -27,7 +29,7 @@ namespace varlen {
 struct PagedSeg {
   int32_t q0, n, sk;   // first packed query row, queries, keys
   int32_t blocks;      // row blocks
-  int64_t per_head;    // tiles of all row blocks of one key head
+  int64_t per_head;    // places of all row blocks of one key head
 };
 
 struct PagedUnit {
@@ -35,6 +37,18 @@ struct PagedUnit {
   int32_t lo, hi;        // keys that some row of the unit sees
   int32_t tile0, tiles;  // first key tile and number of key tiles
 };
+
+// n / d: 64-bit division is a long subroutine, and hardly ever needed here.
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  if (((uint64_t)n | (uint64_t)d) >> 32 == 0) return (int64_t)((uint32_t)n / (uint32_t)d);
+  return n / d;
+}
+
+// CTAs that share `total` places: no more than leave each `least`.
+__device__ __forceinline__ int32_t paged_ctas(int64_t total, int32_t grid, int32_t least) {
+  const int64_t n = quotient(total + least - 1, least);
+  return (int32_t)(n < 1 ? 1 : (n < grid ? n : grid));
+}
 
 // Geometry of a kernel's units: ROWS rows per block, or, with BY_TOKEN, the
 // rows of two halves of whole tokens (ROWS / 2 / group tokens each); TILE keys
@@ -64,6 +78,26 @@ struct PagedGeom {
     u.tiles = u.hi > u.lo ? (u.hi - 1) / TILE + 1 - u.tile0 : 0;
     return u;
   }
+  // Places that a tile and a unit take in the list: one a tile or, with trees, what they
+  // cost: a tile of two halves 5, of one 4 (2.4 and 1.9 us in E4M3, 2.1 and 1.75 in bf16), a
+  // unit's start and end two such tiles; in the kernel for few rows 1 and 3.  For 64 trees
+  // of 16..64 rows, 4 heads a key head, over 1..8192 keys, us, tiles alone, tiles and ends, all
+  // three: E4M3 350, 326, 320, bf16 270, 248, 235; trees of 33..64 336, 301, 300 and 260, 226, 227; of
+  // 1..4 140, 130 and 160, 152.
+  static constexpr int32_t kTilePlaces = TREE && BY_TOKEN ? 5 : 1, kHalfPlaces = TREE && BY_TOKEN ? 4 : 1,
+                           kEndPlaces = TREE ? (BY_TOKEN ? 10 : 3) : 0;
+  __device__ static __forceinline__ int32_t per_tile(const PagedParams& p, const PagedUnit& u) {
+    return kHalfPlaces != kTilePlaces && u.t1 - u.t0 < half_tokens(p) ? kHalfPlaces : kTilePlaces;
+  }
+  __device__ static __forceinline__ int32_t weight(const PagedParams& p, const PagedUnit& u) {
+    return max(u.tiles, 1) * per_tile(p, u) + kEndPlaces;
+  }
+  // CTAs that share a list of `total` places: no more than leave each `least` tiles.
+  __device__ static __forceinline__ int32_t ctas(int64_t total, int32_t grid, int32_t least) {
+    // (with trees no part is shorter than that: each then holds the first place of some tile of
+    // a unit that goes on before and behind it, as the join takes for granted)
+    return paged_ctas(TREE ? max(total - (kTilePlaces * least - 1), (int64_t)1) : total, grid, kTilePlaces * least);
+  }
 };
 
 template <class G>
@@ -77,7 +111,7 @@ __device__ __forceinline__ PagedSeg paged_seg(const PagedParams& p, int32_t b, i
   if ((take == kTakeFew && !few) || (take == kTakeMany && few)) s.n = 0;
   s.blocks = G::blocks(p, s.n);
   s.per_head = 0;
-  for (int32_t i = 0; i < s.blocks; ++i) s.per_head += max(G::unit(p, s.n, s.sk, i).tiles, 1);
+  for (int32_t i = 0; i < s.blocks; ++i) s.per_head += G::weight(p, G::unit(p, s.n, s.sk, i));
   return s;
 }
 
@@ -95,25 +129,14 @@ struct PagedPiece {
 
 // Where a CTA's part begins, shared by its threads.
 struct PagedStart {
-  int64_t total, first, count;  // tiles of the launch; first tile and number of tiles of this CTA
-  int64_t off;                  // first tile's place within segment b
+  int64_t total, first, count;  // places of the launch; first and number of this CTA's
+  int64_t off;                  // the first one's place within segment b
   int32_t b, ctas;              // segment; CTAs that have work
   PagedSeg seg;                 // of segment b
   long long sums[16];
 };
 
-// n / d: 64-bit division is a long subroutine, and hardly ever needed here.
-__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
-  if (((uint64_t)n | (uint64_t)d) >> 32 == 0) return (int64_t)((uint32_t)n / (uint32_t)d);
-  return n / d;
-}
-
-// CTAs that share `total` tiles: no more than leave each `least`.
-__device__ __forceinline__ int32_t paged_ctas(int64_t total, int32_t grid, int32_t least) {
-  const int64_t n = quotient(total + least - 1, least);
-  return (int32_t)(n < 1 ? 1 : (n < grid ? n : grid));
-}
-// First tile of CTA c: the parts have total / ctas tiles, the first total %
+// First place of CTA c: the parts have total / ctas places, the first total %
 // ctas of them one more.
 struct PagedShares {
   int64_t each, more;
@@ -161,7 +184,7 @@ __device__ __forceinline__ void paged_start(PagedStart& st, const PagedParams& p
     if (w < warp) excl += st.sums[w];
     total += st.sums[w];
   }
-  const int32_t ctas = paged_ctas(total, gridDim.x, least);
+  const int32_t ctas = G::ctas(total, gridDim.x, least);
   const bool works = total > 0 && (int32_t)blockIdx.x < ctas;
   const PagedShares shares(total, ctas);
   const int64_t first = works ? shares.first(blockIdx.x) : 0;
@@ -212,56 +235,57 @@ __device__ __forceinline__ void paged_start(PagedStart& st, const PagedParams& p
 template <class G>
 struct PagedWalk {
   PagedSeg s;
-  int32_t b, kh, blk, j, take;
-  int64_t left;
+  int32_t b, kh, blk, at, take;  // at: the part's place within its next unit
+  int64_t left;                  // its places from there on
   __device__ __forceinline__ void init(const PagedStart& st, const PagedParams& p, int32_t take_) {
     take = take_;
     left = st.count;
     b = st.b;
-    kh = blk = j = 0;
+    kh = blk = 0;
+    at = 0;
     if (left <= 0) return;
     s = st.seg;
     int64_t off = st.off;
     kh = (int32_t)quotient(off, s.per_head);
     off -= (int64_t)kh * s.per_head;
     while (true) {
-      const int32_t c = max(G::unit(p, s.n, s.sk, blk).tiles, 1);
-      if (off < c) break;
-      off -= c;
+      const int32_t w = G::weight(p, G::unit(p, s.n, s.sk, blk));
+      if (off < w) break;
+      off -= w;
       ++blk;
     }
-    j = (int32_t)off;
+    at = (int32_t)off;
   }
   __device__ __forceinline__ bool next(const PagedParams& p, PagedPiece& x) {
-    if (left <= 0) return false;
-    while (blk >= s.blocks) {
-      blk = 0;
-      if (s.blocks > 0 && kh + 1 < p.kv_heads) {
-        ++kh;
-        break;
+    while (left > 0) {
+      while (blk >= s.blocks) {
+        blk = 0;
+        if (s.blocks > 0 && kh + 1 < p.kv_heads) {
+          ++kh;
+          break;
+        }
+        if (++b >= p.batch) return false;
+        s = paged_seg<G>(p, b, take);
+        kh = 0;
       }
-      if (++b >= p.batch) return false;
-      s = paged_seg<G>(p, b, take);
-      kh = 0;
-    }
-    x.u = G::unit(p, s.n, s.sk, blk);
-    x.b = b;
-    x.kh = kh;
-    x.blk = blk;
-    x.q0 = s.q0;
-    x.n = s.n;
-    x.sk = s.sk;
-    x.cost = max(x.u.tiles, 1);
-    x.j0 = j;
-    x.j1 = (int32_t)min((int64_t)x.cost, j + left);
-    left -= x.j1 - x.j0;
-    if (x.j1 == x.cost) {
+      x.u = G::unit(p, s.n, s.sk, blk);
+      x.b = b;
+      x.kh = kh;
+      x.blk = blk;
+      x.q0 = s.q0;
+      x.n = s.n;
+      x.sk = s.sk;
+      x.cost = max(x.u.tiles, 1);
+      // the tiles whose first place lies in the part
+      const int32_t w = G::weight(p, x.u), per = G::per_tile(p, x.u), end = (int32_t)min((int64_t)w, at + left);
+      x.j0 = min((at + per - 1) / per, x.cost);
+      x.j1 = min((end + per - 1) / per, x.cost);
+      left -= w - at;  // (0 or less: this is the last)
+      at = 0;
       ++blk;
-      j = 0;
-    } else {
-      j = x.j1;
+      if (x.j0 < x.j1) return true;
     }
-    return true;
+    return false;
   }
 };
 
@@ -348,16 +372,15 @@ __device__ __forceinline__ void paged_refuse(const PagedParams& p, const PagedPa
 
 // Left for the join by the one thread that calls it, for every piece: the
 // units that the CTA holds a part of (its first and its last piece, if any).
+template <class G>
 __device__ __forceinline__ void paged_note(const PagedParams& p, const PagedParts& parts, const PagedStart& st,
-                                           const PagedPiece& x) {
+                                           const PagedWalk<G>& walk, const PagedPiece& x) {
   if (x.whole()) return;
-  // the unit's first and last tile in the launch's list (x is the CTA's last
-  // piece where it begins the unit, its first where it does not)
-  const int64_t begin = x.begins() ? st.first + st.count - x.j1 : st.first - x.j0;
   const PagedShares shares(st.total, st.ctas);
+  const int64_t begin = st.first + st.count - walk.left - G::weight(p, x.u);  // the unit's first place (walk stands behind it)
   const int32_t first = shares.owner(begin);
   put_join(p, parts, 2 * blockIdx.x + (x.begins() ? 1 : 0),
-           PagedJoin{x.b, x.kh, x.blk, first, shares.owner(begin + x.cost - 1) - first + 1});
+           PagedJoin{x.b, x.kh, x.blk, first, shares.owner(begin + (int64_t)(x.cost - 1) * G::per_tile(p, x.u)) - first + 1});
 }
 
 }  // namespace varlen

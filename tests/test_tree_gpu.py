@@ -213,7 +213,8 @@ def _held(va, cache, n):
 def test_a_skipped_load_times_out_and_the_next_call_is_right(va, kind, which, new, columns, load):
     """3: the kernel for few rows, 4: the one for many; the bounded waits run out, the call says so, the context lives on."""
     assert va.varlen_attn_get_device_status() == 0
-    cache, _, _ = C.make_cache([5000, 900], 2, 128, 64, kind, DEV, columns=columns)
+    # (330 tiles in the kernel for many rows: two of them at least in every CTA, the first one's too)
+    cache, _, _ = C.make_cache([20000, 900], 2, 128, 64, kind, DEV, columns=columns)
     q = torch.randn(sum(new), 4, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
     masks = torch.full((sum(new), 4), -1, dtype=torch.int32, device=DEV)
     assert va.varlen_attn_debug_skip_load(which, load) == 0

@@ -556,9 +556,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
           }
         } else if (live) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (in_span(parts.o_span, part + d0 + 4 * i, 16, p.err))
-              *reinterpret_cast<uint4*>(part + d0 + 4 * i) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 4; ++i)  // (a thread has a row of its own: whole sectors)
+            if (in_span(parts.o_span, part + d0 + 8 * i, 32, p.err)) store_sector(part + d0 + 8 * i, &o[8 * i]);
         }
       }
       if (live && whole) {

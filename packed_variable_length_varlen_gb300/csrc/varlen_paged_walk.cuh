@@ -348,6 +348,13 @@ __device__ __forceinline__ void tree_unit_bits(const PagedParams& p, const Paged
     any[k] = __reduce_or_sync(0xffffffffu, any[k]) & bits_between(unit_lo - key0 - 32 * k, x.u.hi - key0 - 32 * k);
 }
 
+// 32 bytes in one store, to an address aligned to them.
+__device__ __forceinline__ void store_sector(float* a, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
 // Entry i of the join's list.
 __device__ __forceinline__ void put_join(const PagedParams& p, const PagedParts& parts, int32_t i, const PagedJoin& u) {
   if (in_span(parts.join_span, parts.join + i, sizeof(PagedJoin), p.err)) parts.join[i] = u;

@@ -137,6 +137,36 @@ def test_trees_in_parts(va, kind, new, lens):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim,heads,kv,new,lens", [(64, 2, 1, [100], [60000]), (96, 6, 2, [40, 33], [30000, 1]), (128, 2, 1, [100], [60000]), (128, 5, 1, [60], [9000])])
+def test_trees_in_many_parts(va, kind, dim, heads, kv, new, lens):
+    """A few units over all SMs, in up to 17, 32 and more than 32 parts each; the causal band over the same cache."""
+    lens = [max(n, m) for n, m in zip(lens, new)]
+    _tree(va, new, lens, heads, kv, dim, 64, kind, extra=2)
+    cache, k, v = C.make_cache(lens, kv, dim, 64, kind, DEV, seed=3)
+    q = torch.randn(sum(new), heads, dim, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).to(DEV)
+    out, lse = va.attention_fwd_paged(q, cache, C.cu_of(new, DEV), causal=True)
+    _ok(va)
+    at = 0
+    for b, n in enumerate(new):
+        seen = torch.arange(lens[b], device=DEV) <= torch.arange(lens[b] - n, lens[b], device=DEV)[:, None]
+        ref = S.attend_tree(q[at:at + n], k[b], v[b], float(torch.tensor(dim ** -0.5, dtype=torch.float32)), seen)
+        C.check_attend(out[at:at + n], lse[:, at:at + n], ref, dim, lens[b])
+        at += n
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,kv,most,ctx,columns", [(8, 1, 40, 300, 1), (6, 2, 90, 700, 1), (16, 2, 12, 900, 1 << 13), (2, 2, 300, 2000, 1)])
+def test_many_units(va, kind, heads, kv, most, ctx, columns):
+    """Short and long units of one and of two halves, empty ones between them: wherever a CTA's part begins and ends."""
+    g = torch.Generator().manual_seed(most)
+    u = torch.rand(2, 48, generator=g).tolist()
+    new = [0 if i % 7 == 3 else int(x * x * most) for i, x in enumerate(u[0])]
+    lens = [n + int(x ** 3 * ctx) for n, x in zip(new, u[1])]
+    _tree(va, new, lens, heads, kv, 64, 16, kind, columns=columns, extra=3)
+    _tree(va, new, lens, heads, kv, 128, 32, kind, columns=columns, left=60, seed=1)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("new,lens,heads", [([12], [100], 1), ([12, 5], [12, 300], 3), ([100], [180], 2), ([200, 70], [200, 500], 4), ([300], [1000], 1)])
 def test_rows_that_nobody_sees(va, kind, new, lens, heads):
     """New rows outside every mask may hold NaN and infinities; rows whose mask is empty (and that have no context) give 0
@@ -186,7 +216,7 @@ def test_more_rows_than_positions(va, kind):
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("n,lens,heads", [(7, 300, 2), (60, 300, 8), (200, 200, 1)])
 def test_a_chain_is_causal(va, kind, n, lens, heads):
-    """Masks of a chain give what the band gives: the same kernels, the same tiles, the same bits."""
+    """Masks of a chain give what the band gives: the same kernels, whose CTAs share the tiles out in another way."""
     cache, _, _ = C.make_cache([lens], 1, 128, 16, kind, DEV)
     q = torch.randn(n, heads, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
     masks = S.pack([range(i + 1) for i in range(n)], -(-n // 32)).to(DEV)

@@ -3,7 +3,7 @@
 //
 // The joins read what the attention kernels wrote just before (out of L2,
 // mostly) and are bound by latency: four dependent loads and a launch, 4 to 6 us
-// for few rows; for many rows up to 40 MB at D = 128, 11 to 17 us.
+// for few rows; for many rows up to 40 MB at D = 128, 10 to 17 us.
 #include "sm103_ptx.cuh"
 #include "varlen_paged.h"
 #include "varlen_paged_walk.cuh"
@@ -66,21 +66,19 @@ __device__ __forceinline__ void join_by_warp(const PagedParams& p, const PagedPa
 #pragma unroll
   for (int w = 16; w >= 1; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
   __syncwarp();
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
   const bool has = lane < D / 4;  // four columns
 #pragma unroll 8
   for (int32_t k = 0; k < u.parts; ++k) {
     const float4* oa = reinterpret_cast<const float4*>(parts.o + at(k) * D) + lane;
     const float4 x = has && in_span(parts.o_span, oa, 16, p.err) ? *oa : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float wk = weight[2 * k];
-    o.x = fmaf(x.x, wk, o.x);
-    o.y = fmaf(x.y, wk, o.y);
-    o.z = fmaf(x.z, wk, o.z);
-    o.w = fmaf(x.w, wk, o.w);
+    const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = fmaf(xs[i], weight[2 * k], o[i]);
   }
   const float inv = join_inv(l);
   uint2* a = reinterpret_cast<uint2*>(p.out + r.q * p.o_rs + (int64_t)r.head * p.o_hs) + lane;
-  if (has && in_span(p.out_span, a, 8, p.err)) *a = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (has && in_span(p.out_span, a, 8, p.err)) *a = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
   if (lane == 0) join_lse(p, r, m, l);
   __syncwarp();  // a warp's next row writes the weights that all its lanes read here
 }

@@ -250,3 +250,38 @@ def test_windows_past_32_bits(va, monkeypatch):
             assert torch.equal(got[0][:n], want[0][:n]) and torch.equal(got[1][:, :n], want[1][:, :n])
     torch.cuda.synchronize()
     assert va.varlen_attn_get_device_status() == 0
+
+
+def test_threads_on_their_own_streams(va):
+    """Calls of four threads at once, each on a stream that is current in its thread: the bits of one alone."""
+    import threading
+    s = _step(va)
+    n = sum(s["new"])
+    rope = va.Rotary(va.rotary_frequencies(64)[0], device=DEV)
+
+    def run(q):
+        got = va.rotary(q, s["k"], rope, s["pos"]) + va.attention_fwd_paged_tree(q, s["cache"], s["cu"], s["masks"])
+        return [got[0], got[1], got[2][:n], got[3][:, :n]]
+    qs = [s["q"] * f for f in (1, 0.5, 2, -1)]
+    want = [run(q) for q in qs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    got = run(qs[i])
+                    stream.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[i], strict=True)):
+                        wrong.append(i)
+        except Exception as e:
+            wrong.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not wrong and not any(t.is_alive() for t in threads)
+    assert va.varlen_attn_get_device_status() == 0

@@ -446,7 +446,9 @@ int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int32_t* cu_seq
  * Attention of drafted trees over the cache: varlen_attn_fwd_paged for
  * segments whose new rows see one another by a mask in place of the band.  The
  * cache already holds the new rows: new row j of segment b (n_b rows) is
- * position seqlens[b] - n_b + j; the positions before them are the context.
+ * position seqlens[b] - n_b + j; the positions before them are the context.  seqlens[b]
+ * may pass what the table can name, as after a plan that found no room there: positions
+ * past the table have no keys, nobody sees them, and rows before it see what they would.
  * Row i (packed row r) sees
  *   - the context: all of it, or, with window_left >= 0, its positions t >=
  *     max(positions[r], seqlens[b] - n_b) - window_left;
@@ -513,7 +515,10 @@ typedef struct {
  * length would exceed the table, get none; their new table entries are -1 (a
  * cache write there is dropped), their rows in pages that they own already are
  * placed, and varlen_attn_cache_trim back to the old length undoes the step for
- * them.  seqlens_out counts their rows all the same, as cu_seqlens does.
+ * them.  seqlens_out counts their rows all the same, as cu_seqlens does, past the
+ * table too: varlen_attn_fwd_paged_tree, _cache_move and _cache_trim take such a length
+ * as it is, while varlen_attn_fwd_paged and _cache_read clamp it, so that the rows of
+ * that sequence would stand too far back there: their results mean nothing.
  *
  * parents (NULL: none): device int32 [total], packed like the rows: the index
  * within its sequence of the row that each one continues, less than its own;

@@ -420,10 +420,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
       // a row that is none sees all keys: what it computes goes nowhere, and its
       // warp is spared the selects
       int32_t key_lo = 0, key_hi = INT32_MAX;
-      const int32_t ctx = x.sk - x.n;
+      const int32_t ctx = x.sk - x.n, edge = min(ctx, x.u.hi);  // (edge: of the keys that every row sees)
       if (live && TREE) {
         key_lo = tree_lo(p, (int64_t)x.q0 + tok, ctx);
-        key_hi = x.sk;
+        key_hi = x.u.hi;
       } else if (live) {
         band_keys(tok, tok, x.n, x.sk, p.win_left, p.win_right, &key_lo, &key_hi);
       }
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         // keys that the row does not see are set to -inf by select
         const int32_t lim = key_hi - (key0 + j * kChunkTile), lim_lo = key_lo - (key0 + j * kChunkTile);
         if (TREE) {
-          if (key0 + (j + 1) * kChunkTile > ctx || __any_sync(0xffffffffu, lim_lo > 0)) {  // new rows, or a window's edge
+          if (key0 + (j + 1) * kChunkTile > edge || __any_sync(0xffffffffu, lim_lo > 0)) {  // new rows, or a window's edge
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t see = live ? tree_bits(p, (int64_t)x.q0 + tok, key0 + j * kChunkTile + 32 * k - ctx) &

@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
         all_lo = max(klo[0], klo[1]);
         all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, 1));
         all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, 2));
-        all_hi = x.sk - x.n;
+        all_hi = min(x.sk - x.n, x.u.hi);
       } else {
         int32_t a, e;
         band_keys(x.u.t1, x.u.t1, x.n, x.sk, p.win_left, p.win_right, &all_lo, &e);
@@ -424,8 +424,8 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int32_t key = key0 + a + r + (e >> 1) * 8, rel = key - (x.sk - x.n);
-                const bool see = rel < 0 ? key >= klo[e & 1]
-                                         : rel < x.n && ((tree_word_at(p, (int64_t)x.q0 + tok[e & 1], rel >> 5) >> (rel & 31)) & 1u) != 0;
+                const bool see = key < x.u.hi && (rel < 0 ? key >= klo[e & 1]
+                                                          : ((tree_word_at(p, (int64_t)x.q0 + tok[e & 1], rel >> 5) >> (rel & 31)) & 1u) != 0);
                 s[e] = see ? s[e] : -INFINITY;
                 any[e >> 1] = any[e >> 1] || see;
               }

@@ -27,7 +27,7 @@
 namespace varlen {
 
 struct PagedSeg {
-  int32_t q0, n, sk;   // first packed query row, queries, keys
+  int32_t q0, n, sk;   // first packed query row, queries, keys (TREE: positions)
   int32_t blocks;      // row blocks
   int64_t per_head;    // places of all row blocks of one key head
 };
@@ -53,7 +53,8 @@ __device__ __forceinline__ int32_t paged_ctas(int64_t total, int32_t grid, int32
 // Geometry of a kernel's units: ROWS rows per block, or, with BY_TOKEN, the
 // rows of two halves of whole tokens (ROWS / 2 / group tokens each); TILE keys
 // per tile.  TREE: the keys are those from where a row at the context's end would
-// begin to see them to the last new row, whichever of them the masks name.
+// begin to see them to the last new row, whichever of them the masks name; sk counts a
+// sequence's positions, its new rows last, although its table may name fewer.
 template <int ROWS, int TILE, bool BY_TOKEN, bool TREE>
 struct PagedGeom {
   __device__ static __forceinline__ int32_t half_tokens(const PagedParams& p) { return ROWS / 2 / p.group; }
@@ -72,8 +73,10 @@ struct PagedGeom {
       u.t0 = (int32_t)(r0 / (uint32_t)p.group);
       u.t1 = (int32_t)(r1 / (uint32_t)p.group);
     }
-    if (TREE) band_keys(0, 0, n, sk, p.win_left, kWinUnbounded, &u.lo, &u.hi);
-    else band_keys(u.t0, u.t1, n, sk, p.win_left, p.win_right, &u.lo, &u.hi);
+    if (TREE) {
+      band_keys(0, 0, n, sk, p.win_left, kWinUnbounded, &u.lo, &u.hi);
+      u.hi = min(u.hi, p.pages.max_pages << p.pages.page_shift);  // (below 2^31)
+    } else band_keys(u.t0, u.t1, n, sk, p.win_left, p.win_right, &u.lo, &u.hi);
     u.tile0 = u.lo / TILE;
     u.tiles = u.hi > u.lo ? (u.hi - 1) / TILE + 1 - u.tile0 : 0;
     return u;
@@ -84,6 +87,7 @@ struct PagedGeom {
   // of 16..64 rows, 4 heads a key head, over 1..8192 keys, us, tiles alone, tiles and ends, all
   // three: E4M3 350, 326, 320, bf16 270, 248, 235; trees of 33..64 336, 301, 300 and 260, 226, 227; of
   // 1..4 140, 130 and 160, 152.
+  static constexpr bool kTree = TREE;
   static constexpr int32_t kTilePlaces = TREE && BY_TOKEN ? 5 : 1, kHalfPlaces = TREE && BY_TOKEN ? 4 : 1,
                            kEndPlaces = TREE ? (BY_TOKEN ? 10 : 3) : 0;
   __device__ static __forceinline__ int32_t per_tile(const PagedParams& p, const PagedUnit& u) {
@@ -106,7 +110,7 @@ __device__ __forceinline__ PagedSeg paged_seg(const PagedParams& p, int32_t b, i
   const int32_t a = clamp_row(p.cu_q[b], p.total_q), e = clamp_row(p.cu_q[b + 1], p.total_q);
   s.q0 = a;
   s.n = max(e - a, 0);
-  s.sk = cache_len(p.pages, b);
+  s.sk = G::kTree ? max(p.pages.seqlens[b], 0) : cache_len(p.pages, b);
   const bool few = s.n * p.group <= kFewRows;  // (total_q * num_heads < 2^31)
   if ((take == kTakeFew && !few) || (take == kTakeMany && few)) s.n = 0;
   s.blocks = G::blocks(p, s.n);
@@ -290,9 +294,10 @@ struct PagedWalk {
 };
 
 // ------------------------------------------------- drafted trees
-// ctx: position of a segment's new row 0 (its keys less its new rows; negative
-// where rows are missing).  A row sees the keys [tree_lo, ctx) and those new rows j,
-// key ctx + j, whose bit its mask has.
+// ctx: position of a segment's new row 0 (its positions less its new rows; negative
+// where rows are missing, past a table that is too short for them).  A row sees the keys
+// [tree_lo, ctx) and those new rows j, key ctx + j, whose bit its mask has, where the table
+// names them (below the unit's hi).
 __device__ __forceinline__ int32_t tree_lo(const PagedParams& p, int64_t row, int32_t ctx) {
   if (p.win_left >= kWinUnbounded) return 0;
   const int32_t* a = p.tree_pos + row;

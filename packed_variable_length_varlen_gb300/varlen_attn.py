@@ -199,8 +199,8 @@ def _load() -> ctypes.CDLL:
 
 def _load_binding(lib):
     """The native binding (csrc/varlen_binding.cpp) over the library's functions, or None: then every call goes by
-    ctypes, with the same results."""
-    if not _build.binding_built():
+    ctypes, with the same results.  One that was built for another header than the library is not loaded."""
+    if not _build.binding_built(lib._name):
         return None
     try:
         loader = importlib.machinery.ExtensionFileLoader("_varlen_binding", _build.BINDING)

@@ -576,10 +576,11 @@ int varlen_attn_cache_move(const varlen_kv_cache* caches, int32_t count, const i
  * pair i is elements (i, i + rotary_dim / 2), or, interleaved, (2 i, 2 i + 1).  The
  * elements behind rotary_dim stay as they are.  rotary_dim: a multiple of 8 from 8
  * to head_dim.  `turns` (device, rotary_dim / 2 entries, 8-byte aligned) holds f_i as a
- * fraction of a turn a position in units of 2^-64, so that the angle of any int32
- * position is exact to 2^-32 of a turn; varlen_attn_rotary_turns (host memory on
- * both sides) makes it from frequencies in radians a position, however these were
- * scaled for long contexts.  The struct is host memory, read during the call only.
+ * fraction of a turn a position in units of 2^-64, and the angle is their whole-number
+ * product, cut to 2^-32 of a turn; varlen_attn_rotary_turns (host memory on
+ * both sides) makes it from frequencies in radians a position (finite, of either sign),
+ * however these were scaled for long contexts, rounded to half a unit below 2^20 radians:
+ * 2^-34 of a turn at the farthest int32 position.  The struct is host memory, read during the call only.
  */
 typedef struct {
   const uint64_t* turns;

@@ -85,6 +85,18 @@ int check_pool(const varlen_page_pool* pool, int32_t batch, PoolView* view) {
 
 bool same(varlen_page_stride a, varlen_page_stride b) { return a.page == b.page && a.row == b.row && a.head == b.head; }
 
+// f / 2 pi in whole 2^-64 turns, rounded once: 1 / 2 pi in two doubles leaves 2^-104 of the
+// quotient, and the two parts of the product are brought into a turn without rounding.
+uint64_t turns_of(double f) {
+  constexpr double kInv = 0x1.45f306dc9c883p-3, kInvLess = -0x1.6b01ec5417056p-57;  // of 1 / 2 pi: the nearest double, the rest's
+  constexpr double kUnits = 18446744073709551616.0;
+  const double a = std::fabs(f), hi = a * kInv, lo = std::fma(a, kInvLess, std::fma(a, kInv, -hi));
+  const double up = std::fmod(hi, 1.0) * kUnits, whole = std::floor(up);
+  const double less = std::rint(std::remainder(lo, 1.0) * kUnits + (up - whole));  // at most 2^63 + 1 either way
+  const uint64_t t = (uint64_t)whole + (less < 0 ? 0 - (uint64_t)-less : (uint64_t)less);  // (modulo a turn)
+  return f < 0 ? 0 - t : t;
+}
+
 int done(cudaError_t e) { return e == cudaSuccess ? VARLEN_OK : cuda_fail(e); }
 
 }  // namespace
@@ -94,11 +106,7 @@ extern "C" int varlen_attn_rotary_turns(const double* frequencies, int32_t count
   if (count > 0 && (frequencies == nullptr || turns == nullptr)) return VARLEN_ERR_NULL;
   for (int32_t i = 0; i < count; ++i)
     if (!std::isfinite(frequencies[i])) return VARLEN_ERR_SHAPE;
-  for (int32_t i = 0; i < count; ++i) {
-    const double t = frequencies[i] / 6.283185307179586476925;
-    const double part = t - std::floor(t);  // [0, 1]: 1 where a tiny negative t rounds up to it
-    turns[i] = part < 1.0 ? (uint64_t)(part * 18446744073709551616.0) : 0;
-  }
+  for (int32_t i = 0; i < count; ++i) turns[i] = turns_of(frequencies[i]);
   return VARLEN_OK;
 }
 

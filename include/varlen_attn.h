@@ -332,7 +332,8 @@ int varlen_attn_fwd_fp8_dense(const void* q, varlen_dense_stride sq, const void*
  * [0, max_pages * page_size], and never follows an entry outside
  * [0, num_pages): a write there, or past the table, is dropped, a read there
  * gives zero rows, and the call records VARLEN_ERR_DEVICE_BOUNDS
- * (varlen_attn_get_device_status).  Sequences may share pages that nothing
+ * (varlen_attn_get_device_status); _fwd_paged_tree and _cache_move, which come behind
+ * a plan, say below how they take lengths past the table and entries of -1.  Sequences may share pages that nothing
  * writes.
  *
  * type VARLEN_CACHE_BF16: bf16 elements, k_scale = v_scale = NULL.
@@ -457,6 +458,8 @@ int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int32_t* cu_seq
  *     own bit is clear does not see itself.
  * A row that sees nothing gets O = 0 and LSE = -inf.  Rows of the cache that no
  * row of a segment sees may hold anything, NaN included, new ones too.
+ * Table entries of -1, which varlen_attn_cache_plan leaves where it has no page, read
+ * as zero rows without an error; other entries that name no page are recorded.
  * masks: device uint32 [total_q][mask_words], as varlen_attn_cache_plan writes
  * it, mask_words >= 1; positions: device int32 [total_q], read only when
  * window_left >= 0 (then not NULL).  All other arguments, the workspace
@@ -515,10 +518,14 @@ typedef struct {
  * length would exceed the table, get none; their new table entries are -1 (a
  * cache write there is dropped), their rows in pages that they own already are
  * placed, and varlen_attn_cache_trim back to the old length undoes the step for
- * them.  seqlens_out counts their rows all the same, as cu_seqlens does, past the
- * table too: varlen_attn_fwd_paged_tree, _cache_move and _cache_trim take such a length
- * as it is, while varlen_attn_fwd_paged and _cache_read clamp it, so that the rows of
- * that sequence would stand too far back there: their results mean nothing.
+ * them.  That is an ordinary outcome, which `unplaced` tells: no call that names a
+ * plan's slots, masks or kept rows records an error for it (varlen_attn_cache_write
+ * and varlen_attn_fwd_paged, which know no plan, do, and so does a later plan whose
+ * rows fall behind such an entry).  seqlens_out counts their rows all the same, as
+ * cu_seqlens does, past the table too: varlen_attn_fwd_paged_tree, _cache_move and
+ * _cache_trim take such a length as it is, while varlen_attn_fwd_paged and _cache_read
+ * clamp it, so that the rows of that sequence would stand too far back there: their
+ * results mean nothing.
  *
  * parents (NULL: none): device int32 [total], packed like the rows: the index
  * within its sequence of the row that each one continues, less than its own;
@@ -558,7 +565,8 @@ int varlen_attn_cache_trim(const varlen_page_pool* pool, const int32_t* lens, co
  * within its n_b rows of cu_seqlens, i <= kept[..] < n_b: ascending indices are)
  * becomes its new row i, in K, in V and in their scales.  Entries outside that
  * range move nothing and record VARLEN_ERR_DEVICE_BOUNDS; rows whose position would be
- * negative are passed over.  seqlens counts all n_b rows, before and after: the
+ * negative, lies past the table or in an entry of -1 (the plan found it no place) are
+ * passed over.  seqlens counts all n_b rows, before and after: the
  * rest goes with varlen_attn_cache_trim.  `caches` is a host array of `count`
  * caches (layers; at most 1024) of one shape, type and strides over one table and
  * one seqlens (VARLEN_ERR_SHAPE otherwise), none of them twice; sequences that

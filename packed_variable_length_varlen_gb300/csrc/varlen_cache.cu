@@ -53,7 +53,7 @@ __device__ __forceinline__ Place place_of(const CacheParams& p, int32_t row, int
     if (p.err != nullptr) atomicOr(p.err, (unsigned int)kErrBounds);
     return x;
   }
-  x.page = page_at(p.pages, b, x.pos >> p.pages.page_shift, p.err);
+  x.page = page_at<false>(p.pages, b, x.pos >> p.pages.page_shift, p.err);
   x.row = x.pos & (p.pages.page_size - 1);
   return x;
 }

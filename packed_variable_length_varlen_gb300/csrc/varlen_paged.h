@@ -53,12 +53,14 @@ __device__ __forceinline__ int32_t cache_len(const PageView& c, int32_t b) {
 }
 
 // Page that holds positions [i << page_shift, ...) of sequence b, 0 <= i <
-// max_pages; num_pages (no page: recorded as an error) for an entry that
-// names none.
+// max_pages; num_pages (no page) for an entry that names none, recorded as an
+// error unless it is the -1 of a plan that had no page to give (PLANNED: calls that
+// come behind a plan, for which that is an ordinary outcome).
+template <bool PLANNED>
 __device__ __forceinline__ int32_t page_at(const PageView& c, int32_t b, int32_t i, unsigned int* err) {
   const int32_t id = c.table[(int64_t)b * c.table_stride + i];
   if ((uint32_t)id < (uint32_t)c.num_pages) return id;
-  if (err != nullptr) atomicOr(err, (unsigned int)kErrBounds);
+  if (err != nullptr && !(PLANNED && id == -1)) atomicOr(err, (unsigned int)kErrBounds);
   return c.num_pages;
 }
 

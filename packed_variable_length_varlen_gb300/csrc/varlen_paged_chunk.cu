@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
           const int32_t key = (x.u.tile0 + j) * kChunkTile + (piece << box_shift);
           int32_t page = p.pages.num_pages;
           if (loads && key < x.u.hi && key + (1 << box_shift) > x.u.lo)
-            page = page_at(p.pages, x.b, key >> p.pages.page_shift, p.err);
+            page = page_at<TREE>(p.pages, x.b, key >> p.pages.page_shift, p.err);
           const int32_t row = key & (p.pages.page_size - 1);
 #pragma unroll
           for (int which = 0; which < 2; ++which, ++pos) {

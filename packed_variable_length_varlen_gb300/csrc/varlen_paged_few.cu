@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, few_ctas(E4M3))
         const int32_t key = (x.u.tile0 + j) * C::KT + (piece << box_shift);
         int32_t page = p.pages.num_pages;
         if (loads && key < x.u.hi && key + (1 << box_shift) > x.u.lo)
-          page = page_at(p.pages, x.b, key >> p.pages.page_shift, p.err);
+          page = page_at<TREE>(p.pages, x.b, key >> p.pages.page_shift, p.err);
         const int32_t row = key & (p.pages.page_size - 1);
 #pragma unroll
         for (int which = 0; which < 2; ++which, ++pos) {

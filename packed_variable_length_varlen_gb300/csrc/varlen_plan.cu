@@ -451,12 +451,8 @@ __global__ void __launch_bounds__(kMoveThreads) varlen_move_kernel(const __grid_
     const int64_t at = start + i;
     page = p.pages.num_pages;
     row = (int32_t)(at & (p.pages.page_size - 1));
-    if (at < 0) return;
-    if ((at >> p.pages.page_shift) >= p.pages.max_pages) {
-      record_error(p.err, kErrBounds);
-      return;
-    }
-    page = page_at(p.pages, b, (int32_t)(at >> p.pages.page_shift), p.err);
+    if (at < 0 || (at >> p.pages.page_shift) >= p.pages.max_pages) return;  // (the plan found it no place)
+    page = page_at<true>(p.pages, b, (int32_t)(at >> p.pages.page_shift), p.err);
   };
   for (int32_t i0 = 0; i0 < kept; i0 += kMoveRows) {  // CTA-uniform
     if (threadIdx.x < 32) {

@@ -159,3 +159,73 @@ def test_lengths_past_the_table(va, kind, heads, length):
         seen = torch.ones(hi - lo, keys, dtype=torch.bool, device=DEV)
         ref = S.attend_tree(q[lo:hi], k[b], v[b], float(torch.tensor(128 ** -0.5, dtype=torch.float32)), seen)
         C.check_attend(out[lo:hi], lse[:, lo:hi], ref, 128, keys)
+
+
+# ------------------------------------------------------------------ too few pages
+
+SHORT = [
+    # (positions before the step, new rows, table's width, page, free pages): who gets none, from the first whose running need
+    # is above them on (the others that need none keep all their rows)
+    ([10, 60, 14, 33, 30], [7, 40, 5, 4, 9], 8, 16, 2),
+    ([0, 100, 5], [3, 60, 2], 12, 16, 0),
+    ([130, 7, 250], [200, 9, 60], 16, 32, 4),
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,kv", [(1, 1), (8, 2)])
+@pytest.mark.parametrize("old,new,width,page,free", SHORT)
+def test_a_step_short_of_pages(va, kind, heads, kv, old, new, width, page, free):
+    """Sequences that get no pages are an ordinary outcome: plan, write, trees, move and trim leave no error, rows without
+    a place read as zeros, and the others' results are what they are."""
+    s = _Step(va, kind, old, new, width, page, heads, kv, 64, free=free)
+    _ok(va)
+    lost, table = s.plan.unplaced.tolist(), s.table.tolist()
+    assert max(lost) > 0 and min(lost) == 0 or free == 0
+    for b, n in enumerate(new):
+        assert lost[b] == sum(s.place(b, old[b] + i) < 0 for i in range(n))
+        assert (-1 in table[b]) == (lost[b] > 0)
+    s.attend()
+    _ok(va)
+    s.attend(20)
+    _ok(va)
+    s.keep([sorted({0, n // 3, n - 1} if b % 2 or lost[b] else {0, min(2, n - 1)}) for b, n in enumerate(new)])
+    _ok(va)
+
+
+def test_the_same_step_undone(va):
+    """Nothing kept: lengths, stack and count are as before the step."""
+    old, new, width, page, free = SHORT[0]
+    s = _Step(va, "bf16", old, new, width, page, 1, 1, 64, free=free)
+    s.keep([[]] * len(old))
+    _ok(va)
+    assert s.seqlens.tolist() == old and s.pool.free_count.item() == free and s.pool.free_pages[:free].tolist() == s.stack
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads", [1, 32])
+@pytest.mark.parametrize("bad", [-2, -2147483648, 1 << 20])
+def test_other_entries_are_reported(va, kind, heads, bad):
+    """An entry that is no page and not the plan's -1 is an error in the trees and in move, as it was; the causal band and the
+    packed write, which have no plan, report -1 too."""
+    cache, _, _ = C.make_cache([60], 1, 64, 16, kind, DEV)
+    q = torch.randn(4, heads, 64, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    masks, cu = torch.full((4, 1), -1, dtype=torch.int32, device=DEV), C.cu_of([4], DEV)
+    for entry, want in ((-1, 0), (bad, va.VARLEN_ERR_DEVICE_BOUNDS)):
+        cache.block_table[0, 3] = entry
+        va.attention_fwd_paged_tree(q, cache, cu, masks, max_seqlen_q=4)
+        _ok(va, want)
+        va.cache_move(cache, cu, _ints([[0, 2]]), _ints([2]))
+        _ok(va, want)
+    cache.block_table[0, 3] = -1
+    va.attention_fwd_paged(q, cache, cu, max_seqlen_q=4, causal=True)
+    _ok(va, va.VARLEN_ERR_DEVICE_BOUNDS)
+    va.cache_write(cache, q[:, :1], q[:, :1], cu)
+    _ok(va, va.VARLEN_ERR_DEVICE_BOUNDS)
+
+
+def test_moves_past_the_table_are_passed_over(va):
+    """Rows that the plan could not place past the table's end go nowhere and come from nowhere, without an error."""
+    s = _Step(va, "bf16", [70, 0], [40, 6], 5, 16, 2, 2, 64)
+    s.keep([[0, 4, 9, 10, 30, 39], [1, 3, 5]])
+    _ok(va)

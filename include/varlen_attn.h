@@ -456,6 +456,10 @@ int varlen_attn_fwd_paged(const void* q, varlen_stride sq, const int32_t* cu_seq
  *   - new row j exactly if bit j % 32 of masks[r * mask_words + j / 32] is set
  *     and j < n_b (bits past the last word are 0), itself included: a row whose
  *     own bit is clear does not see itself.
+ * The window cuts the context alone: it takes nothing from the mask.  A model whose
+ * window counts a row's own tree too, as varlen_attn_fwd_window does of a chain, has
+ * masks without the bits of rows further than window_left above (varlen_attn_cache_plan
+ * names every row above); paths of at most window_left + 1 rows have none.
  * A row that sees nothing gets O = 0 and LSE = -inf.  Rows of the cache that no
  * row of a segment sees may hold anything, NaN included, new ones too.
  * Table entries of -1, which varlen_attn_cache_plan leaves where it has no page, read

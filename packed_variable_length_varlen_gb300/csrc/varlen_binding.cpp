@@ -4,9 +4,9 @@
 // Python attributes and ctypes for each of them.
 //
 // A small call is the host's.  A step of 16 rows, one call after another, through
-// ctypes and through this: rotary_cache_write 15.5 -> 5.0 us (its kernel 2.4),
-// cache_plan 5.5 -> 3.5 (2.9), cache_move and cache_trim 11.5 -> 6.0, tree attention
-// 25 -> 18 (its kernels 18).  Everything here is a shortcut for calls that are as usual: where
+// ctypes and through this: rotary_cache_write 15.9 -> 4.9 us (its kernel 2.5),
+// cache_plan 5.5 -> 3.4 (3.1), cache_move and cache_trim 12.0 -> 6.3, tree attention
+// of 52 rows 27 -> 14.7 (its kernels 14.6).  Everything here is a shortcut for calls that are as usual: where
 // anything is not (a wrong type or shape, another device than the current one, a
 // stream of the caller's own), a function returns NotImplemented before it has done
 // anything, and varlen_attn.py goes its own way, which also words the refusals.  A

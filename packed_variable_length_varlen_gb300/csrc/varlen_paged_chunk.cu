@@ -41,7 +41,8 @@
 // for all masks, and softmax and conversion read their piece where it lies instead of keeping
 // it in registers: 64 trees of 64 rows, 4 heads a key head, over 8192 keys 458 us in bf16
 // and 501 in E4M3, where the causal band takes 470 and 515 (a second select in the
-// softmax and pieces in registers: 488 and 641).  256 rows of 7 heads over 77000 bf16 keys 464-519.
+// softmax and pieces in registers: 488 and 641).  256 rows of 7 heads over 77000 bf16
+// keys 456-474 from a graph, 497-523 a call.
 //
 // P is rounded to bf16, V's type, which the second product asks for: each weight
 // is off by at most 2^-9 of its binade, O by 2e-3 to 2.4e-3 relative to 64 bits

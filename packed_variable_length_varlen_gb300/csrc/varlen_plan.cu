@@ -296,6 +296,9 @@ __global__ void __launch_bounds__(kRowThreads) varlen_plan_trees_kernel(const __
 
 // One CTA: the pages that come back, from the last sequence's last to the first's
 // first, form a list; entries that name a page are numbered and go onto the stack.
+// Made for the few pages that come back behind a step (3.7 us for 256 sequences of 4 pages); many
+// are taken THREADS at a time, a dependent load and two barriers each: 64 sequences of 64 pages
+// 15 us, 256 of 512 184 us.
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) varlen_trim_kernel(const __grid_constant__ TrimParams p) {
   __shared__ long long sums[32];

@@ -22,7 +22,10 @@
 // Measured: 262144 rows of 40 heads of 128, 629 us, 7.2 TB/s (a plain copy moves 6.8);
 // 29012 rows of 32 heads of 96, half of each turned, 58 us, 6.4 TB/s; 7493 rows of 32 heads,
 // with 8 of K and of V into a bf16 cache, 32 us, 5.8 TB/s; 16 rows of those into an E4M3
-// cache 2.4 us, the launch and two memory latencies.  With angles worked out by every
+// cache 2.4 us, the launch and two memory latencies; 60000 rows of 32 heads, with 8 of K and V,
+// from cold 237 us into a bf16 cache, 6.2 TB/s, and 270 into an E4M3 one, 5.0 TB/s.  Few heads a row
+// leave most of a warp's places empty: 65536 rows of 8 + 1 heads of 64 take 52 us, 2.9 TB/s, and
+// 75 and 92 with the write, bf16 and E4M3; of 1 + 1 heads of 128 48, 1.4 TB/s, and 71 and 89.  With angles worked out by every
 // lane the first was 667.
 #include <algorithm>
 
@@ -39,7 +42,8 @@ constexpr int kWarps = kRotaryThreads / 32;
 constexpr int kPairs = 64;  // of a head, at most
 // Lanes up to which each takes one head, for the sake of a short chain; one head and
 // four, us: 16 rows of 40 heads of 128 2.2 and 2.6, 256 rows 2.7 and 2.9, 512 (163840 lanes)
-// 3.3 and 3.1, 1024 5.2 and 4.3.
+// 3.3 and 3.1, 1024 5.2 and 4.3.  (Set by the rows' form; the write of 512 rows of 48 heads,
+// 196608 lanes, takes 4.6 and 4.9, so that its border lies somewhat higher.)
 constexpr int kFewLanes = 1 << 17;
 
 // V bf16 elements.

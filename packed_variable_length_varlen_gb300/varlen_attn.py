@@ -912,7 +912,10 @@ def attention_fwd_paged_tree(q, cache, cu_seqlens_q, masks, max_seqlen_q=0, scal
     rows: each sees the context and those new rows of its segment whose bit its
     row of masks ([rows, words] int32, as StepPlan has them) has set.  With
     window_left >= 0 the context is seen that far back from positions ([rows]
-    int32); everything else as in attention_fwd_paged."""
+    int32); everything else as in attention_fwd_paged.  The window takes nothing
+    from the masks: where a path has more than window_left + 1 rows, a row sees those
+    of its path that attention_fwd_paged's window would hide from it, unless the
+    caller clears their bits (cache_plan sets one for every row above)."""
     if NATIVE is not None and stream is None and out is None and lse is None and workspace is None:
         got = NATIVE.attention_fwd_paged_tree(cache.at, cache.batch, q, cu_seqlens_q, masks, max_seqlen_q, scale, window_left,
                                               positions)
@@ -1102,7 +1105,10 @@ def rotary_frequencies(rotary_dim, base=10000.0, stretch=1.0, how="ramp", traine
                 that the slowest pair is stretched whole and the fastest not at all;
       "ramp"    pairs that turn at least `high` times within `trained` positions are
                 kept, those that turn at most `low` times are stretched, linear in
-                the number of turns between; scale 0.1 ln(stretch) + 1."""
+                the number of turns between; scale 0.1 ln(stretch) + 1.
+    Models differ in such ramps (linear in the pair's index instead of in its turns,
+    scale 1 instead): theirs are frequencies and a scale of the caller's own, which
+    Rotary takes as they are."""
     if rotary_dim < 2 or rotary_dim % 2 or base <= 0 or stretch <= 0 or how not in ("linear", "base", "ramp"):
         raise ValueError("rotary_dim must be even, base and stretch positive, how linear, base or ramp")
     i = torch.arange(0, rotary_dim, 2, dtype=torch.float64)

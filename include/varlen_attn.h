@@ -333,8 +333,8 @@ int varlen_attn_fwd_fp8_dense(const void* q, varlen_dense_stride sq, const void*
  * [0, num_pages): a write there, or past the table, is dropped, a read there
  * gives zero rows, and the call records VARLEN_ERR_DEVICE_BOUNDS
  * (varlen_attn_get_device_status); _fwd_paged_tree and _cache_move, which come behind
- * a plan, say below how they take lengths past the table and entries of -1.  Sequences may share pages that nothing
- * writes.
+ * a plan, say below how they take lengths past the table and entries of -1.
+ * Sequences may share pages that nothing writes.
  *
  * type VARLEN_CACHE_BF16: bf16 elements, k_scale = v_scale = NULL.
  * type VARLEN_CACHE_E4M3: one-byte E4M3 codes and a bf16 scale for every

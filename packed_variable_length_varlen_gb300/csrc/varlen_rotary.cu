@@ -25,8 +25,8 @@
 // cache 2.4 us, the launch and two memory latencies; 60000 rows of 32 heads, with 8 of K and V,
 // from cold 237 us into a bf16 cache, 6.2 TB/s, and 270 into an E4M3 one, 5.0 TB/s.  Few heads a row
 // leave most of a warp's places empty: 65536 rows of 8 + 1 heads of 64 take 52 us, 2.9 TB/s, and
-// 75 and 92 with the write, bf16 and E4M3; of 1 + 1 heads of 128 48, 1.4 TB/s, and 71 and 89.  With angles worked out by every
-// lane the first was 667.
+// 75 and 92 with the write, bf16 and E4M3; of 1 + 1 heads of 128 48, 1.4 TB/s, and 71 and 89.
+// With angles worked out by every lane the first was 667.
 #include <algorithm>
 
 #include "sm103_ptx.cuh"
